@@ -274,6 +274,89 @@ MOE_API moe_status_t moe_backward(const moe_layer_desc *desc, const uint16_t *x,
                                   const float *dy, float *dx, float *dWr, float *dW_gate_up, float *dW_down,
                                   float *dWsh_gate_up, float *dWsh_down, void *ws, size_t ws_bytes, void *stream);
 
+/* ---- Training around the layer: token rows sorted by expert and back, and orthogonalised
+ * updates of the expert weights. The row type of an array is one of these. */
+typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dtype_t;
+
+/* Token rows sorted by expert: the differentiable form of an expert-parallel dispatch and return
+ * (moe_ep_pack and moe_combine are the layer's own forward-only forms). T tokens with k entries
+ * each; entry n = t*k + j goes to expert topk_idx[t, j] and is DROPPED when that id is
+ * outside [0, E) (padding, or an expert of another rank: k may exceed E). Any H >= 1; rows of
+ * `dtype`, contiguous, aligned to their element (16-byte aligned rows are the fast case);
+ * k <= 32, E <= 1024, H <= 2^22, T*k < 2^31 - 2^20 (MOE_ERR_UNSUPPORTED beyond; k: MOE_ERR_INVALID_ARG).
+ * Sorted arrays hold T*k rows. Arrays of one call must not overlap. */
+typedef struct {
+    int32_t T;     /* tokens */
+    int32_t H;     /* row width */
+    int32_t E;     /* experts */
+    int32_t k;     /* entries per token */
+    int32_t dtype; /* moe_dtype_t of the rows */
+} moe_token_desc;
+
+/* Device workspace of moe_sort_tokens (contents need not be initialised). */
+MOE_API moe_status_t moe_sort_workspace_size(const moe_token_desc *desc, size_t *bytes);
+
+/* slot_of [T, k] int32: the entry's place among the kept entries ordered by (expert, n), -1 for
+ * a dropped entry; offsets [E+1] int32: expert e's places are [offsets[e], offsets[e+1]);
+ * x_sorted [T*k, H]: x_sorted[slot_of[t, j]] = x[t]; rows from offsets[E] on are not written.
+ * Exact and deterministic. ws 16-byte aligned. T = 0: offsets (if not NULL) is zeroed. */
+MOE_API moe_status_t moe_sort_tokens(const moe_token_desc *desc, const void *x, const int32_t *topk_idx,
+                                     void *x_sorted, int32_t *offsets, int32_t *slot_of, void *ws, size_t ws_bytes,
+                                     void *stream);
+
+/* Gradient of the sort: dx[t] = sum_j dx_sorted[slot_of[t, j]] over the kept entries (0 without
+ * any), summed in fp32 in rank order and rounded once. dx [T, H] is overwritten. */
+MOE_API moe_status_t moe_sort_tokens_backward(const moe_token_desc *desc, const void *dx_sorted,
+                                              const int32_t *slot_of, void *dx, void *stream);
+
+/* Rows back to their tokens, weighted: y[t] = sum_j topk_w[t, j] * y_sorted[slot_of[t, j]] + add[t]
+ * over the kept entries, in fp32 in rank order, rounded once. topk_w [T, k] fp32 or NULL (1);
+ * add [T, H] (e.g. the shared expert's output) or NULL (0). y [T, H] is overwritten. A slot
+ * outside [0, T*k) counts as dropped here and in the gradient; what is dropped is not read. */
+MOE_API moe_status_t moe_unsort_tokens(const moe_token_desc *desc, const void *y_sorted, const int32_t *slot_of,
+                                       const float *topk_w, const void *add, void *y, void *stream);
+
+/* Gradient of the weighted unsort (that of `add` is dy itself):
+ *   dy_sorted[slot_of[t, j]] = topk_w[t, j] * dy[t]   rows that no entry owns are not written
+ *   dtopk_w[t, j] = <dy[t], y_sorted[slot_of[t, j]]>  fp32, fixed order; 0 for a dropped entry
+ * Either output may be NULL, y_sorted when dtopk_w is. Slots must be distinct, as
+ * moe_sort_tokens makes them: two entries with one slot would both write its row. */
+MOE_API moe_status_t moe_unsort_tokens_backward(const moe_token_desc *desc, const void *dy, const void *y_sorted,
+                                                const int32_t *slot_of, const float *topk_w, void *dy_sorted,
+                                                float *dtopk_w, void *stream);
+
+/* Orthogonalised update of n matrices [rows, cols] (for the layer: W_gate_up as 2E matrices
+ * [I, H], W_down as E matrices [H, I]) by Newton-Schulz products, as the Muon optimiser
+ * does. Per matrix:
+ *   u = grad; with momentum: m <- beta*m + grad, u = nesterov ? grad + beta*m : m
+ *   X = u / (|u|_F + eps); `steps` times X <- a*X + (b*A + c*A*A)*X, A = X*X^T (the shorter
+ *   side's Gram matrix; X from the right when rows > cols); out = bf16(scale * X)
+ * The customary coefficients are a, b, c = 3.4445, -4.7750, 2.0315 with 5 steps. Products run
+ * in fp16 with fp32 accumulation, what is not an operand in about 22 bits. A zero matrix gives zero (eps
+ * > 0); a matrix with a NaN or an infinity gives NaN, the others are unaffected. */
+typedef struct {
+    int32_t n, rows, cols;
+    int32_t dtype; /* moe_dtype_t of grad: MOE_DTYPE_F32 or MOE_DTYPE_BF16 */
+    int32_t steps; /* 1 .. 32 */
+    float a, b, c;
+    float eps;     /* >= 0 */
+    float scale;
+    float beta;    /* used when momentum is given */
+    int32_t nesterov;
+} moe_orthogonalize_desc;
+
+/* MOE_ERR_UNSUPPORTED: rows or cols above 16384, n above 65535, fp16 gradients, or coefficients
+ * whose iterates leave the operands' range (singular values growing past 7.9, or b*s^2 +
+ * c*s^4 past 31). The workspace holds as many matrices as fit 2 GiB (at least one), 12 bytes per
+ * element of X and A; larger stacks are worked off in equal chunks. */
+MOE_API moe_status_t moe_orthogonalize_workspace_size(const moe_orthogonalize_desc *desc, size_t *bytes);
+
+/* grad [n, rows, cols] of dtype; momentum [n, rows, cols] fp32, updated in place, or NULL; out
+ * [n, rows, cols] bf16 bit patterns, overwritten; all contiguous and aligned to their elements,
+ * ws 256-byte aligned. n = 0 is a no-op. Deterministic. */
+MOE_API moe_status_t moe_orthogonalize(const moe_orthogonalize_desc *desc, const void *grad, float *momentum,
+                                       uint16_t *out, void *ws, size_t ws_bytes, void *stream);
+
 /* moe_forward without a caller-provided workspace. The pages have no counterpart: this
  * entry point exists for callers that cannot allocate device memory at call time, such
  * as a serving runtime whose device memory is already handed to a fixed pool, a

@@ -26,7 +26,12 @@ EXPORTS = ["moe_status_string", "moe_workspace_size", "moe_router", "moe_permute
            "moe_combine", "moe_forward", "moe_check_device", "moe_set_wait_limit_ns", "moe_set_stage_events",
            "moe_forward_noalloc", "moe_forward_with_ids", "moe_forward_fp8", "moe_backward",
            "moe_backward_workspace_size", "moe_ep_pack", "moe_ep_experts", "moe_shared_expert",
-           "moe_host_workspace_size", "moe_forward_host"]
+           "moe_host_workspace_size", "moe_forward_host", "moe_sort_workspace_size", "moe_sort_tokens",
+           "moe_sort_tokens_backward", "moe_unsort_tokens", "moe_unsort_tokens_backward",
+           "moe_orthogonalize_workspace_size", "moe_orthogonalize"]
+
+# moe_dtype_t of the row and gradient arrays
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
 class MoeError(RuntimeError):
@@ -40,6 +45,18 @@ class LayerDesc(ctypes.Structure):
                 ("I", ctypes.c_int32), ("Is", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("norm_expert_weight", ctypes.c_int32), ("limit_routed", ctypes.c_float),
                 ("limit_shared", ctypes.c_float), ("deterministic", ctypes.c_int32)]
+
+
+class TokenDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class OrthogonalizeDesc(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("steps", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float),
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("beta", ctypes.c_float),
+                ("nesterov", ctypes.c_int32)]
 
 
 def desc_of(shape, T=None, deterministic=False) -> LayerDesc:
@@ -85,6 +102,17 @@ def lib():
         L.moe_shared_expert.argtypes = [dp] + [vp] * 5 + [sz, vp]
         L.moe_host_workspace_size.argtypes = [dp, ctypes.POINTER(sz)]
         L.moe_forward_host.argtypes = [dp, ctypes.c_int32] + [vp] * 11 + [sz, vp]
+        tp, op = ctypes.POINTER(TokenDesc), ctypes.POINTER(OrthogonalizeDesc)
+        L.moe_sort_workspace_size.argtypes = [tp, ctypes.POINTER(sz)]
+        L.moe_sort_tokens.argtypes = [tp] + [vp] * 6 + [sz, vp]
+        L.moe_sort_tokens_backward.argtypes = [tp] + [vp] * 4
+        L.moe_unsort_tokens.argtypes = [tp] + [vp] * 6
+        L.moe_unsort_tokens_backward.argtypes = [tp] + [vp] * 7
+        L.moe_orthogonalize_workspace_size.argtypes = [op, ctypes.POINTER(sz)]
+        L.moe_orthogonalize.argtypes = [op] + [vp] * 4 + [sz, vp]
+        for name in ("moe_sort_workspace_size", "moe_sort_tokens", "moe_sort_tokens_backward", "moe_unsort_tokens",
+                     "moe_unsort_tokens_backward", "moe_orthogonalize_workspace_size", "moe_orthogonalize"):
+            getattr(L, name).restype = i32
         for name in ("moe_ep_pack", "moe_ep_experts", "moe_shared_expert", "moe_host_workspace_size",
                      "moe_forward_host"):
             getattr(L, name).restype = i32
@@ -244,4 +272,47 @@ def moe_forward_host(desc, n_batches, x_host, Wr, bias, W_gate_up, W_down, Wsh_g
     _check("moe_forward_host", lib().moe_forward_host(
         ctypes.byref(desc), int(n_batches), _p(x_host), _p(Wr), _p(bias), _p(W_gate_up), _p(W_gate_up_scale),
         _p(W_down), _p(W_down_scale), _p(Wsh_gate_up), _p(Wsh_down), _p(y_host), _p(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_sort_workspace_size(desc: TokenDesc) -> int:
+    out = ctypes.c_size_t(0)
+    _check("moe_sort_workspace_size", lib().moe_sort_workspace_size(ctypes.byref(desc), ctypes.byref(out)))
+    return out.value
+
+
+def moe_sort_tokens(desc, x, topk_idx, x_sorted, offsets, slot_of, ws, stream=None):
+    """Rows of x sorted by expert, with the places and offsets (entries with ids outside [0, E) dropped)."""
+    _check("moe_sort_tokens", lib().moe_sort_tokens(
+        ctypes.byref(desc), _p(x), _p(topk_idx), _p(x_sorted), _p(offsets), _p(slot_of), _p(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_sort_tokens_backward(desc, dx_sorted, slot_of, dx, stream=None):
+    _check("moe_sort_tokens_backward", lib().moe_sort_tokens_backward(
+        ctypes.byref(desc), _p(dx_sorted), _p(slot_of), _p(dx), _stream(stream)))
+
+
+def moe_unsort_tokens(desc, y_sorted, slot_of, topk_w, add, y, stream=None):
+    _check("moe_unsort_tokens", lib().moe_unsort_tokens(
+        ctypes.byref(desc), _p(y_sorted), _p(slot_of), _p(topk_w), _p(add), _p(y), _stream(stream)))
+
+
+def moe_unsort_tokens_backward(desc, dy, y_sorted, slot_of, topk_w, dy_sorted, dtopk_w, stream=None):
+    _check("moe_unsort_tokens_backward", lib().moe_unsort_tokens_backward(
+        ctypes.byref(desc), _p(dy), _p(y_sorted), _p(slot_of), _p(topk_w), _p(dy_sorted), _p(dtopk_w),
+        _stream(stream)))
+
+
+def moe_orthogonalize_workspace_size(desc: OrthogonalizeDesc) -> int:
+    out = ctypes.c_size_t(0)
+    _check("moe_orthogonalize_workspace_size",
+           lib().moe_orthogonalize_workspace_size(ctypes.byref(desc), ctypes.byref(out)))
+    return out.value
+
+
+def moe_orthogonalize(desc, grad, momentum, out, ws, stream=None):
+    """Orthogonalised updates of a stack of matrices (momentum updated in place, or None)."""
+    _check("moe_orthogonalize", lib().moe_orthogonalize(
+        ctypes.byref(desc), _p(grad), _p(momentum), _p(out), _p(ws),
         0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))

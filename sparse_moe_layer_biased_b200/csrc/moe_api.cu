@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "../../include/moe_b200.h"
+#include "context.h"
 #include "internal.h"
 
 namespace {
@@ -519,6 +520,33 @@ moe_status_t check_bwd_desc(const moe_layer_desc *d)
 }
 
 }  // namespace
+
+namespace moe {
+
+int device_context(DeviceContext &out)
+{
+    DeviceInfo di;
+    const moe_status_t st = device_info(di);
+    if (st == MOE_OK)
+        out = DeviceContext{di.num_sms, wait_cfg(di)};
+    return st;
+}
+
+bool map_stack_f16(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t n, int64_t pitch,
+                   int64_t mat_pitch, uint32_t box_rows)
+{
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(n)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch) * 2, static_cast<cuuint64_t>(mat_pitch) * 2};
+    const cuuint32_t box[3] = {64, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+}  // namespace moe
 
 extern "C" {
 
