@@ -12,6 +12,9 @@ import os
 
 import torch
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # MOE_B200_DEBUG=1 loads the debug build (device-side range checks, MOE_ERR_DEVICE_BOUNDS)
 DEBUG = os.environ.get("MOE_B200_DEBUG", "0") == "1"
@@ -133,7 +136,9 @@ def _p(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream() without the Stream object around it, which
+        # costs as much host time (3 us) as a kernel launch
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

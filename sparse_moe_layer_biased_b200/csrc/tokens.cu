@@ -30,8 +30,10 @@ constexpr int kMaxExperts = 1024;
 // ---------------------------------------------------------------------------------- sort
 // Small calls, one launch: an entry's place is the number of entries with a smaller key
 // id * N + n (N = T * k entries in all), so every block counts for its own token, with no
-// dependence between blocks: N compares per entry in place of two more launches and their hand-over.
-constexpr int kSmallEntries = 4096;
+// dependence between blocks: N compares per entry in place of another launch and the hand-over. Measured
+// against the two launches below: 512 entries 2.6 us, where the two launches alone take longer; 3108
+// entries of 2 KB rows 6.2 against 5.4 us; 4096 entries of 8 KB rows 9.8 against 10.3 us.
+constexpr int kSmallEntries = 2048;
 constexpr int kRowThreads = 128;
 constexpr int kDroppedKey = 0x7fffffff;
 
@@ -40,19 +42,23 @@ __device__ __forceinline__ int entry_key(int id, int n, int E, int N)
     return static_cast<unsigned>(id) < static_cast<unsigned>(E) ? id * N + n : kDroppedKey;
 }
 
-// Row t of x (units of U) to the rows slots[0..k) of out; columns [c0, c1) of the row. Every
-// load of a piece is issued before its k copies are stored.
+// A row (units of U) to the rows slots[0..k) of x_sorted, columns [c0, c1). Every load of a piece
+// (V units per thread) is issued before its k copies are stored; load() may run before the
+// slots are known.
 template <typename U>
-__device__ __forceinline__ void scatter_row(const U *__restrict__ src, U *__restrict__ out, int64_t units, int64_t c0,
-                                            int64_t c1, const int *slots, int k)
-{
-    constexpr int V = 4;
-    for (int64_t c = c0 + threadIdx.x; c < c1; c += V * kRowThreads) {
-        U v[V];
+struct RowCopy {
+    static constexpr int V = sizeof(U) >= 8 ? 4 : 8;
+    U v[V];
+    __device__ __forceinline__ void load(const U *__restrict__ src, int64_t c, int64_t c1)
+    {
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (c + i * kRowThreads < c1)
                 v[i] = src[c + i * kRowThreads];
+    }
+    __device__ __forceinline__ void store(U *__restrict__ out, int64_t units, int64_t c, int64_t c1, const int *slots,
+                                          int k) const
+    {
         for (int j = 0; j < k; ++j) {
             const int64_t s = slots[j];
             if (s < 0)
@@ -64,7 +70,7 @@ __device__ __forceinline__ void scatter_row(const U *__restrict__ src, U *__rest
                     dst[c + i * kRowThreads] = v[i];
         }
     }
-}
+};
 
 // Block 0 of the small sort: offsets[0..E] from a histogram in shared memory.
 __device__ __forceinline__ void small_offsets(const int32_t *__restrict__ idx, int N, int E, int32_t *hist,
@@ -130,6 +136,11 @@ __global__ void __launch_bounds__(kRowThreads)
         return;
     }
     const int t = blockIdx.x - 1;
+    const U *src = x + static_cast<int64_t>(t) * units;
+    const int64_t c1 = (blockIdx.y + 1) * chunk < units ? (blockIdx.y + 1) * chunk : units;
+    int64_t c = blockIdx.y * chunk + threadIdx.x;
+    RowCopy<U> row;
+    row.load(src, c, c1);  // on its way while the places are counted
     for (int n = threadIdx.x; n < N; n += kRowThreads)
         tab[n] = entry_key(idx[n], n, E, N);
     __syncthreads();
@@ -165,15 +176,145 @@ __global__ void __launch_bounds__(kRowThreads)
         }
         __syncthreads();
     }
-    const int64_t c0 = blockIdx.y * chunk;
-    const int64_t c1 = c0 + chunk < units ? c0 + chunk : units;
-    scatter_row(x + static_cast<int64_t>(t) * units, x_sorted, units, c0, c1, slots, k);
+    for (;;) {
+        row.store(x_sorted, units, c, c1, slots, k);
+        c += RowCopy<U>::V * kRowThreads;
+        if (c >= c1)
+            break;
+        row.load(src, c, c1);
+    }
 }
 
-// Larger calls, three launches. count: block b owns `per` consecutive entries, its warps
-// consecutive parts of them; an entry's rank among the block's entries of its expert comes from
-// __match_any_sync (32 entries at a time) on per-warp counters. scan: hist[b][e] becomes the
-// first place of block b's entries of expert e. place: slot = hist[b][e] + rank, and the rows.
+// Larger calls, one launch for the places and one for the rows. The places: one cluster of
+// kPlaceCtas CTAs, CTA c owning consecutive entries, its warps consecutive parts of them in R rounds
+// of 32, all in registers. An entry's rank among its warp's earlier entries of the same expert
+// comes from a warp-wide comparison on per-warp counters; counters are summed over warps, over the CTAs
+// through distributed shared memory, and scanned over experts.
+constexpr int kPlaceCtas = 8;
+constexpr int kPlaceThreads = 1024;
+constexpr int kPlaceWarps = kPlaceThreads / 32;
+constexpr int kMaxRounds = 4;  // R: up to kPlaceCtas * kPlaceThreads * kMaxRounds = 131072 entries
+
+// Lanes of the warp that hold the same value of `bits` bits. A ballot per bit: __match_any_sync, which
+// answers the same, takes about 70 cycles of a unit that the SM's warps share (131072 entries on eight
+// SMs: 24 us with it, 16 us with ballots).
+__device__ __forceinline__ unsigned same_value(int v, int bits)
+{
+    unsigned m = 0xFFFFFFFFu;
+    for (int b = 0; b < bits; ++b) {
+        const bool on = v >> b & 1;
+        const unsigned vote = __ballot_sync(0xFFFFFFFFu, on);
+        m &= on ? vote : ~vote;
+    }
+    return m;
+}
+
+// Exclusive prefix over the block's 1024 threads.
+__device__ __forceinline__ int block_exclusive(int v, int *warp_sums)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = v;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o)
+            incl += u;
+    }
+    if (lane == 31)
+        warp_sums[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        const int s = warp_sums[lane];
+        int si = s;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, si, o);
+            if (lane >= o)
+                si += u;
+        }
+        warp_sums[lane] = si - s;
+    }
+    __syncthreads();
+    return warp_sums[warp] + incl - v;
+}
+
+template <int R>
+__global__ void __launch_bounds__(kPlaceThreads)
+    sort_places_kernel(const int32_t *__restrict__ idx, int N, int E, int32_t *__restrict__ offsets,
+                       int32_t *__restrict__ slot_of)
+{
+    allow_dependents();
+    extern __shared__ int32_t cnt[];    // [kPlaceWarps][E]
+    int32_t *total = cnt + kPlaceWarps * E;  // [E] this CTA's counts, read by its peers
+    __shared__ int warp_sums[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int cta = static_cast<int>(cluster_ctarank());
+    const int base = (cta * kPlaceWarps + warp) * R * 32 + lane;
+    const int bits = 32 - __clz(E);  // of the values 0 .. E
+    int id[R], rank[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int n = base + r * 32;
+        id[r] = n < N ? idx[n] : -1;
+    }
+    for (int i = threadIdx.x; i < kPlaceWarps * E; i += kPlaceThreads)
+        cnt[i] = 0;
+    __syncthreads();
+    int32_t *mine = cnt + warp * E;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const bool kept = static_cast<unsigned>(id[r]) < static_cast<unsigned>(E);
+        const unsigned m = same_value(kept ? id[r] : E, bits);
+        const int before = kept ? mine[id[r]] : 0;
+        __syncwarp();
+        if (kept && lane == 31 - __clz(m))
+            mine[id[r]] = before + __popc(m);
+        __syncwarp();
+        rank[r] = kept ? before + __popc(m & ((1u << lane) - 1u)) : -1;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kPlaceThreads) {  // E <= kPlaceThreads: one pass
+        int run = 0;
+#pragma unroll
+        for (int w = 0; w < kPlaceWarps; ++w) {
+            const int c = cnt[w * E + e];
+            cnt[w * E + e] = run;
+            run += c;
+        }
+        total[e] = run;
+    }
+    cluster_sync_all();
+    int below = 0, all = 0;
+    const int e = threadIdx.x;
+    if (e < E) {
+        const uint32_t local = smem_u32(total + e);
+#pragma unroll
+        for (int c = 0; c < kPlaceCtas; ++c) {
+            const int v = dsmem_ld_s32(dsmem_addr(local, c));
+            below += c < cta ? v : 0;
+            all += v;
+        }
+    }
+    const int start = block_exclusive(all, warp_sums);
+    cluster_sync_all();  // the peers have read this CTA's counts: they become the expert's base here
+    if (e < E) {
+        total[e] = start + below;
+        if (cta == 0) {
+            offsets[e] = start;
+            if (e == E - 1)
+                offsets[E] = start + all;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int n = base + r * 32;
+        if (n < N)
+            slot_of[n] = rank[r] < 0 ? -1 : total[id[r]] + mine[id[r]] + rank[r];
+    }
+}
+
+// Still larger ones, two launches for the places. count: block b owns `per` consecutive entries,
+// ranked within the block as above; scan: hist[b][e] becomes the first place of block b's entries of
+// expert e. The rows' launch adds the two.
 constexpr int kCountThreads = 256;
 constexpr int kCountWarps = kCountThreads / 32;
 constexpr int kCountBlocks = 128;  // most blocks of the count
@@ -183,11 +324,13 @@ __global__ void __launch_bounds__(kCountThreads)
     sort_count_kernel(const int32_t *__restrict__ idx, int64_t N, int E, int per, int32_t *__restrict__ hist,
                       int32_t *__restrict__ rank)
 {
+    allow_dependents();
     extern __shared__ int32_t cnt[];  // [kCountWarps][E]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int i = threadIdx.x; i < kCountWarps * E; i += kCountThreads)
         cnt[i] = 0;
     __syncthreads();
+    const int bits = 32 - __clz(E);
     const int per_warp = per / kCountWarps;  // a multiple of 32
     const int64_t begin = static_cast<int64_t>(blockIdx.x) * per + warp * per_warp;
     int32_t *mine = cnt + warp * E;
@@ -195,7 +338,7 @@ __global__ void __launch_bounds__(kCountThreads)
         const int64_t n = begin + i + lane;
         const int id = n < N ? idx[n] : -1;
         const bool kept = static_cast<unsigned>(id) < static_cast<unsigned>(E);
-        const unsigned m = __match_any_sync(0xFFFFFFFFu, kept ? id : E + lane);
+        const unsigned m = same_value(kept ? id : E, bits);
         const int before = kept ? mine[id] + __popc(m & ((1u << lane) - 1u)) : -1;
         __syncwarp();
         if (kept && lane == 31 - __clz(m))
@@ -232,6 +375,8 @@ __global__ void __launch_bounds__(1024)
     __shared__ int part[1024];
     __shared__ int start[kMaxExperts / kScanCtas];
     __shared__ int cta_total;
+    allow_dependents();
+    dependency_wait();
     const int groups = 1024 / ep_pad;
     const int le = threadIdx.x % ep_pad, g = threadIdx.x / ep_pad;
     const int e = static_cast<int>(cluster_ctarank()) * ep + le;
@@ -292,23 +437,42 @@ __global__ void __launch_bounds__(1024)
     cluster_sync_all();  // no CTA leaves while a peer may still read its total
 }
 
-template <typename U>
+// Block t copies token t's row; its loads are on their way before the places are. kFinal: slot_of
+// holds the places already (sort_places_kernel). What the launch before wrote is read through
+// pointers without __restrict__: such loads could move above the wait.
+template <typename U, bool kFinal>
 __global__ void __launch_bounds__(kRowThreads)
-    sort_place_kernel(const U *__restrict__ x, const int32_t *__restrict__ idx, int k, int E, int per,
-                      const int32_t *__restrict__ hist, const int32_t *__restrict__ rank, int64_t units,
-                      U *__restrict__ x_sorted, int32_t *__restrict__ slot_of)
+    sort_rows_kernel(const U *__restrict__ x, const int32_t *__restrict__ idx, int k, int E, int per,
+                     const int32_t *hist, const int32_t *rank, int64_t units, U *__restrict__ x_sorted,
+                     int32_t *slot_of)
 {
     __shared__ int slots[kMaxK];
     const int64_t t = blockIdx.x;
+    const U *src = x + t * units;
+    int64_t c = threadIdx.x;
+    RowCopy<U> row;
+    row.load(src, c, units);
+    dependency_wait();
     if (threadIdx.x < k) {
         const int64_t n = t * k + threadIdx.x;
-        const int r = rank[n];
-        const int s = r < 0 ? -1 : hist[n / per * E + idx[n]] + r;
+        int s;
+        if (kFinal) {
+            s = slot_of[n];
+        } else {
+            const int r = rank[n];
+            s = r < 0 ? -1 : hist[n / per * E + idx[n]] + r;
+            slot_of[n] = s;
+        }
         slots[threadIdx.x] = s;
-        slot_of[n] = s;
     }
     __syncthreads();
-    scatter_row(x + t * units, x_sorted, units, 0, units, slots, k);
+    for (;;) {
+        row.store(x_sorted, units, c, units, slots, k);
+        c += RowCopy<U>::V * kRowThreads;
+        if (c >= units)
+            break;
+        row.load(src, c, units);
+    }
 }
 
 struct SortPlan {
@@ -330,6 +494,39 @@ SortPlan sort_plan(int64_t N, int E)
     return p;
 }
 
+template <int R>
+cudaError_t launch_places_r(const int32_t *idx, int N, int E, int32_t *offsets, int32_t *slot_of, cudaStream_t stream)
+{
+    const int smem = (kPlaceWarps + 1) * E * 4;
+    const cudaError_t err =
+        cudaFuncSetAttribute(sort_places_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess)
+        return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kPlaceCtas);
+    cfg.blockDim = dim3(kPlaceThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kPlaceCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sort_places_kernel<R>, idx, N, E, offsets, slot_of);
+}
+
+cudaError_t launch_places(const int32_t *idx, int N, int E, int32_t *offsets, int32_t *slot_of, cudaStream_t stream)
+{
+    const int round = kPlaceCtas * kPlaceThreads;
+    if (N <= round)
+        return launch_places_r<1>(idx, N, E, offsets, slot_of, stream);
+    if (N <= 4 * round)
+        return launch_places_r<4>(idx, N, E, offsets, slot_of, stream);
+    return launch_places_r<kMaxRounds>(idx, N, E, offsets, slot_of, stream);
+}
+
 template <typename U>
 cudaError_t launch_sort(const void *x, const int32_t *idx, int T, int k, int E, int64_t row_bytes, void *x_sorted,
                         int32_t *offsets, int32_t *slot_of, void *ws, int num_sms, cudaStream_t stream)
@@ -348,6 +545,14 @@ cudaError_t launch_sort(const void *x, const int32_t *idx, int T, int k, int E, 
         sort_small_kernel<U><<<grid, kRowThreads, 0, stream>>>(xs, idx, T, k, E, units, chunk, out, offsets, slot_of);
         return cudaGetLastError();
     }
+    if (N <= static_cast<int64_t>(kPlaceCtas) * kPlaceThreads * kMaxRounds) {
+        cudaError_t err = launch_places(idx, static_cast<int>(N), E, offsets, slot_of, stream);
+        if (err != cudaSuccess)
+            return err;
+        return launch_dependent(sort_rows_kernel<U, true>, dim3(T), kRowThreads, 0, stream, 1, xs, idx, k, E, 1,
+                                static_cast<const int32_t *>(nullptr), static_cast<const int32_t *>(nullptr), units,
+                                out, slot_of);
+    }
     const SortPlan p = sort_plan(N, E);
     int32_t *hist = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + p.hist);
     int32_t *rank = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + p.rank);
@@ -359,22 +564,13 @@ cudaError_t launch_sort(const void *x, const int32_t *idx, int T, int k, int E, 
     int ep_pad = 1;
     while (ep_pad < ep)
         ep_pad *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kScanCtas);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kScanCtas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, sort_scan_kernel, hist, p.nb, E, ep, ep_pad, offsets);
+    err = launch_dependent(sort_scan_kernel, dim3(kScanCtas), 1024, 0, stream, kScanCtas, hist, p.nb, E, ep, ep_pad,
+                           offsets);
     if (err != cudaSuccess)
         return err;
-    sort_place_kernel<U><<<T, kRowThreads, 0, stream>>>(xs, idx, k, E, p.per, hist, rank, units, out, slot_of);
-    return cudaGetLastError();
+    return launch_dependent(sort_rows_kernel<U, false>, dim3(T), kRowThreads, 0, stream, 1, xs, idx, k, E, p.per,
+                            static_cast<const int32_t *>(hist), static_cast<const int32_t *>(rank), units, out,
+                            slot_of);
 }
 
 // --------------------------------------------------------------------- rows in fp32 and back
@@ -395,26 +591,22 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// y[t] = add[t] + sum_j w[t, j] rows[slot_of[t, j]] (w NULL: 1, add NULL: 0) for columns of one
-// kRowThreads * VEC wide chunk. A slot outside [0, rows) contributes nothing.
-template <typename S, int VEC>
+// y[t] = add[t] + sum_j w[t, j] rows[slot_of[t, j]] (w NULL: 1, add NULL: 0) for packs [c0, c0 +
+// chunk) of the row; a slot outside [0, N) contributes nothing. The chunks of a token are
+// neighbours in the grid, so that a row's 8 KB are read at one time: with the tokens innermost DRAM saw
+// 2 KB pieces: 4.8 against 6.6 TB/s over 1.2 GB. kOne: k <= 8, slots and weights stay in registers.
+template <typename S, int VEC, bool kOne>
 __global__ void __launch_bounds__(kRowThreads)
     unsort_kernel(const S *__restrict__ rows, const int32_t *__restrict__ slot_of, const float *__restrict__ w,
-                  const S *__restrict__ add, int k, int64_t N, int H, S *__restrict__ y)
+                  const S *__restrict__ add, int k, int64_t N, int H, int chunk, int chunks, S *__restrict__ y)
 {
     using P = Pack<S, VEC>;
-    const int64_t t = blockIdx.x;
-    const int col = (blockIdx.y * kRowThreads + threadIdx.x) * VEC;
-    if (col >= H)
-        return;
-    float acc[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i)
-        acc[i] = 0.0f;
-    for (int j0 = 0; j0 < k; j0 += 8) {
-        P r[8];
-        int64_t s[8];
-        float wj[8];
+    const int64_t t = blockIdx.x / chunks;
+    const int c0 = (blockIdx.x - static_cast<int>(t) * chunks) * chunk;
+    const int c1 = c0 + chunk < H / VEC ? c0 + chunk : H / VEC;
+    int s[8];
+    float wj[8];
+    auto fetch = [&](int j0) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             s[j] = -1;
@@ -423,49 +615,128 @@ __global__ void __launch_bounds__(kRowThreads)
                 s[j] = slot_of[t * k + j0 + j];
                 if (w)
                     wj[j] = w[t * k + j0 + j];
+                if (s[j] >= N)
+                    s[j] = -1;
             }
-            if (s[j] >= N)
-                s[j] = -1;
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (s[j] >= 0)
-                r[j] = *reinterpret_cast<const P *>(rows + s[j] * H + col);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (s[j] >= 0)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    acc[i] = fmaf(wj[j], to_f32(r[j].v[i]), acc[i]);
-    }
-    if (add) {
-        const P a = *reinterpret_cast<const P *>(add + t * H + col);
+    };
+    if (kOne)
+        fetch(0);
+    for (int c = c0 + threadIdx.x; c < c1; c += kRowThreads) {
+        const int64_t col = static_cast<int64_t>(c) * VEC;
+        P a;
+        if (add)
+            a = *reinterpret_cast<const P *>(add + t * H + col);
+        float acc[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
-            acc[i] += to_f32(a.v[i]);
-    }
-    P o;
+            acc[i] = 0.0f;
+        for (int j0 = 0; j0 < k; j0 += 8) {
+            if (!kOne)
+                fetch(j0);
+            P r[8];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i)
-        o.v[i] = from_f32<S>(acc[i]);
-    *reinterpret_cast<P *>(y + t * H + col) = o;
+            for (int j = 0; j < 8; ++j)
+                if (s[j] >= 0)
+                    r[j] = *reinterpret_cast<const P *>(rows + static_cast<int64_t>(s[j]) * H + col);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (s[j] >= 0)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        acc[i] = fmaf(wj[j], to_f32(r[j].v[i]), acc[i]);
+            if (kOne)
+                break;
+        }
+        if (add)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                acc[i] += to_f32(a.v[i]);
+        P o;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            o.v[i] = from_f32<S>(acc[i]);
+        *reinterpret_cast<P *>(y + t * H + col) = o;
+    }
 }
 
-// Entries j0 .. j0 + JB of token t (block (t, j0 / JB)): their rows of dy_sorted and, through a
-// block-wide sum in a fixed order, their dw.
+// The gradient of the unsort: per entry its row of dy_sorted and, through a sum in a fixed order,
+// its dw. Many entries of narrow rows: a warp per entry, the entries of a token in one block or
+// neighbouring ones, so that dy comes from L1 for all but the first; no barrier, U packs of both
+// rows in flight per lane. Against the blocks below: 4500 entries of 4092 bytes 8.1 against 17 us; 32768 entries
+// of 8 KB 109 against 99 us.
 constexpr int kBackThreads = 256;
 
-template <typename S, int VEC, int JB>
+template <typename S, int VEC>
 __global__ void __launch_bounds__(kBackThreads)
     unsort_backward_kernel(const S *__restrict__ dy, const S *__restrict__ rows, const int32_t *__restrict__ slot_of,
                            const float *__restrict__ w, int k, int64_t N, int H, S *__restrict__ drows,
                            float *__restrict__ dw)
 {
     using P = Pack<S, VEC>;
+    constexpr int U = sizeof(P) >= 16 ? 4 : 8;
+    const int lane = threadIdx.x & 31;
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * (kBackThreads / 32) + (threadIdx.x >> 5);
+    if (n >= N)
+        return;
+    const int64_t s = slot_of[n];
+    float acc = 0.0f;
+    if (s >= 0 && s < N) {
+        const float wn = w ? w[n] : 1.0f;
+        const int64_t t = static_cast<uint32_t>(n) / static_cast<uint32_t>(k);
+        const P *g_row = reinterpret_cast<const P *>(dy + t * H);
+        const P *r_row = reinterpret_cast<const P *>(rows + s * H);
+        P *d_row = reinterpret_cast<P *>(drows + s * H);
+        const int packs = H / VEC;
+        for (int c = lane; c < packs; c += U * 32) {
+            P g[U], r[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c + u * 32 < packs) {
+                    g[u] = g_row[c + u * 32];
+                    if (dw)
+                        r[u] = r_row[c + u * 32];
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c + u * 32 < packs) {
+                    if (dw)
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i)
+                            acc = fmaf(to_f32(g[u].v[i]), to_f32(r[u].v[i]), acc);
+                    if (drows) {
+                        P o;
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i)
+                            o.v[i] = from_f32<S>(wn * to_f32(g[u].v[i]));
+                        d_row[c + u * 32] = o;
+                    }
+                }
+        }
+    }
+    if (!dw)
+        return;
+    for (int o = 16; o > 0; o >>= 1)
+        acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
+    if (lane == 0)
+        dw[n] = acc;
+}
+
+// JB entries of one token per block. Eight for wide rows of many tokens: 4 KB of dy, then 4 KB
+// of up to eight rows at a time, longer runs of reads and of writes in DRAM than from a warp per
+// entry. One for few entries, so that they fill the SMs (dy is then read k times): 512 entries 3.2 us, a warp
+// per entry or eight entries per block 4.5 us and more.
+template <typename S, int VEC, int JB>
+__global__ void __launch_bounds__(kBackThreads)
+    unsort_backward_token_kernel(const S *__restrict__ dy, const S *__restrict__ rows,
+                                 const int32_t *__restrict__ slot_of, const float *__restrict__ w, int k, int64_t N,
+                                 int H, S *__restrict__ drows, float *__restrict__ dw)
+{
+    using P = Pack<S, VEC>;
     __shared__ float part[kBackThreads / 32][JB];
     const int64_t t = blockIdx.x;
     const int j0 = blockIdx.y * JB;
-    int64_t s[JB];
+    int s[JB];
     float wj[JB], acc[JB];
 #pragma unroll
     for (int j = 0; j < JB; ++j) {
@@ -476,18 +747,18 @@ __global__ void __launch_bounds__(kBackThreads)
             s[j] = slot_of[t * k + j0 + j];
             if (w)
                 wj[j] = w[t * k + j0 + j];
+            if (s[j] >= N)
+                s[j] = -1;
         }
-        if (s[j] >= N)
-            s[j] = -1;
     }
-    for (int64_t col = static_cast<int64_t>(threadIdx.x) * VEC; col < H; col += kBackThreads * VEC) {
+    for (int col = threadIdx.x * VEC; col < H; col += kBackThreads * VEC) {
         const P g = *reinterpret_cast<const P *>(dy + t * H + col);
         P r[JB];
         if (dw) {
 #pragma unroll
             for (int j = 0; j < JB; ++j)
                 if (s[j] >= 0)
-                    r[j] = *reinterpret_cast<const P *>(rows + s[j] * H + col);
+                    r[j] = *reinterpret_cast<const P *>(rows + static_cast<int64_t>(s[j]) * H + col);
 #pragma unroll
             for (int j = 0; j < JB; ++j)
                 if (s[j] >= 0)
@@ -503,7 +774,7 @@ __global__ void __launch_bounds__(kBackThreads)
 #pragma unroll
                     for (int i = 0; i < VEC; ++i)
                         o.v[i] = from_f32<S>(wj[j] * to_f32(g.v[i]));
-                    *reinterpret_cast<P *>(drows + s[j] * H + col) = o;
+                    *reinterpret_cast<P *>(drows + static_cast<int64_t>(s[j]) * H + col) = o;
                 }
         }
     }
@@ -538,14 +809,27 @@ int pack_bytes(int64_t row_bytes, int elem, std::initializer_list<const void *> 
     return elem;
 }
 
+// Packs of a row per block and blocks per row: whole rows, but for few tokens as many pieces of at
+// least one pack per thread as give every SM sixteen blocks.
+void split_row(int64_t packs, int T, int num_sms, int &chunk, int &chunks)
+{
+    int64_t pieces = (16 * static_cast<int64_t>(num_sms) + T - 1) / T;
+    const int64_t most = (packs + kRowThreads - 1) / kRowThreads;
+    pieces = pieces < most ? pieces : most;
+    chunk = static_cast<int>(((packs + pieces - 1) / pieces + 31) / 32 * 32);
+    chunks = static_cast<int>((packs + chunk - 1) / chunk);
+}
+
 template <typename S, int VEC>
 cudaError_t unsort_vec(const void *rows, const int32_t *slot_of, const float *w, const void *add, int T, int k, int H,
-                       void *y, cudaStream_t stream)
+                       void *y, int num_sms, cudaStream_t stream)
 {
-    const dim3 grid(T, (H + kRowThreads * VEC - 1) / (kRowThreads * VEC));
-    unsort_kernel<S, VEC><<<grid, kRowThreads, 0, stream>>>(
+    int chunk, chunks;
+    split_row(H / VEC, T, num_sms, chunk, chunks);
+    auto kernel = k <= 8 ? unsort_kernel<S, VEC, true> : unsort_kernel<S, VEC, false>;
+    kernel<<<static_cast<unsigned>(static_cast<int64_t>(T) * chunks), kRowThreads, 0, stream>>>(
         static_cast<const S *>(rows), slot_of, w, static_cast<const S *>(add), k, static_cast<int64_t>(T) * k, H,
-        static_cast<S *>(y));
+        chunk, chunks, static_cast<S *>(y));
     return cudaGetLastError();
 }
 
@@ -556,12 +840,16 @@ cudaError_t unsort_backward_vec(const void *dy, const void *rows, const int32_t 
     const S *g = static_cast<const S *>(dy), *r = static_cast<const S *>(rows);
     S *d = static_cast<S *>(drows);
     const int64_t N = static_cast<int64_t>(T) * k;
-    // few tokens: a block per entry, so that the entries fill the SMs (dy is then read k times)
-    if (T < 4 * num_sms)
-        unsort_backward_kernel<S, VEC, 1><<<dim3(T, k), kBackThreads, 0, stream>>>(g, r, slot_of, w, k, N, H, d, dw);
-    else
-        unsort_backward_kernel<S, VEC, 8>
+    if (N < 8 * static_cast<int64_t>(num_sms))
+        unsort_backward_token_kernel<S, VEC, 1>
+            <<<dim3(T, k), kBackThreads, 0, stream>>>(g, r, slot_of, w, k, N, H, d, dw);
+    else if (VEC * sizeof(S) == 16 && H / VEC >= kBackThreads && T >= 2 * num_sms)
+        unsort_backward_token_kernel<S, VEC, 8>
             <<<dim3(T, (k + 7) / 8), kBackThreads, 0, stream>>>(g, r, slot_of, w, k, N, H, d, dw);
+    else
+        unsort_backward_kernel<S, VEC>
+            <<<static_cast<unsigned>((N + kBackThreads / 32 - 1) / (kBackThreads / 32)), kBackThreads, 0, stream>>>(
+                g, r, slot_of, w, k, N, H, d, dw);
     return cudaGetLastError();
 }
 
@@ -689,7 +977,7 @@ moe_status_t moe_sort_tokens(const moe_token_desc *desc, const void *x, const in
 moe_status_t moe_unsort_tokens(const moe_token_desc *desc, const void *y_sorted, const int32_t *slot_of,
                                const float *topk_w, const void *add, void *y, void *stream)
 {
-    const moe_status_t st = check_tokens(desc);
+    moe_status_t st = check_tokens(desc);
     if (st != MOE_OK)
         return st;
     if (desc->T == 0)
@@ -700,11 +988,14 @@ moe_status_t moe_unsort_tokens(const moe_token_desc *desc, const void *y_sorted,
     if (!aligned_to(y_sorted, elem) || !aligned_to(y, elem) || !aligned_to(add, elem) || !aligned_to(slot_of, 4) ||
         !aligned_to(topk_w, 4))
         return MOE_ERR_UNSUPPORTED;
+    DeviceContext dc;
+    if ((st = static_cast<moe_status_t>(device_context(dc))) != MOE_OK)
+        return st;
     const int bytes = pack_bytes(static_cast<int64_t>(desc->H) * elem, elem, {y_sorted, add, y});
     return launched(by_type(desc->dtype, bytes, [&](auto tag) {
         using V = decltype(tag);
         return unsort_vec<typename V::type, V::vec>(y_sorted, slot_of, topk_w, add, desc->T, desc->k, desc->H, y,
-                                                    static_cast<cudaStream_t>(stream));
+                                                    dc.num_sms, static_cast<cudaStream_t>(stream));
     }));
 }
 

@@ -23,7 +23,7 @@ from . import _abi
 
 def check_tensor(t, name: str, shape, dtype, device) -> None:
     """ValueError unless t is a contiguous tensor of this shape, type and device."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {device} is wanted, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}"
                          f"{'' if t.is_contiguous() else ' (not contiguous)'}")
@@ -46,6 +46,7 @@ class TokenSorter:
             raise ValueError(f"rows of {dtype} are not supported")
         self.max_tokens, self.H, self.E, self.k, self.dtype = max_tokens, H, E, k, dtype
         self._code = _abi.DTYPES[dtype]
+        self._last = None  # the latest call's descriptor
         nbytes = _abi.moe_sort_workspace_size(self._desc(max_tokens))
         device = torch.device(device)
         if device.type == "cuda" and device.index is None:
@@ -54,7 +55,10 @@ class TokenSorter:
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
 
     def _desc(self, T: int) -> _abi.TokenDesc:
-        return _abi.TokenDesc(T, self.H, self.E, self.k, self._code)
+        d = self._last
+        if d is None or d.T != T:
+            d = self._last = _abi.TokenDesc(T, self.H, self.E, self.k, self._code)
+        return d
 
     def _rows(self, t: torch.Tensor, name: str, rows: int) -> None:
         check_tensor(t, name, (rows, self.H), self.dtype, self.device)

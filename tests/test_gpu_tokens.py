@@ -16,7 +16,10 @@ BF, HF, FP = torch.bfloat16, torch.float16, torch.float32
 CASES = [
     (1, 4096, 288, 8, BF, 0.0), (1, 1, 1, 1, FP, 0.0), (3, 7, 5, 2, HF, 0.3), (64, 4096, 288, 8, BF, 0.0),
     (64, 256, 16, 4, BF, 0.2), (33, 1290, 60, 6, HF, 0.2), (5, 24, 1024, 32, FP, 0.1), (128, 40, 1, 32, HF, 0.4),
-    (512, 72, 352, 8, BF, 0.0), (513, 72, 352, 8, BF, 0.1),          # the last small sort and the first large one
+    (512, 72, 352, 8, BF, 0.0), (513, 72, 352, 8, BF, 0.1),
+    (256, 40, 352, 8, BF, 0.1), (257, 40, 352, 8, BF, 0.1),          # 2048 entries: the last sort of one launch
+    (1024, 16, 33, 8, HF, 0.1), (1025, 16, 33, 8, HF, 0.1),          # 8192: one round a warp
+    (4096, 8, 1024, 8, BF, 0.1), (4097, 8, 1024, 8, BF, 0.1),        # 32768: the last sort of two launches
     (1500, 1023, 40, 3, FP, 0.2), (777, 514, 16, 7, FP, 0.1), (2001, 100, 1024, 9, HF, 0.0),
     (4096, 513, 3, 4, BF, 1.0), (200, 64, 7, 5, FP, 1.0), (9000, 32, 288, 8, BF, 0.05), (700, 8200, 11, 8, BF, 0.5),
     (40000, 8, 1000, 8, HF, 0.02),
