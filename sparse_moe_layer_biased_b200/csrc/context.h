@@ -14,10 +14,10 @@ struct DeviceContext {
 int device_context(DeviceContext &out);
 
 // 16-bit floating-point tensor map of a stack [n, rows, cols] with a row pitch and a matrix
-// pitch in elements (128-byte swizzle, boxes of 64 columns x box_rows rows of one matrix,
-// elements outside a matrix read as zero). False if the driver rejects it.
+// pitch in elements (boxes of box_cols columns x box_rows rows of one matrix, 64 columns with
+// 128-byte swizzle or 32 with 64-byte swizzle; elements outside a matrix read as zero). False if the driver rejects it.
 bool map_stack_f16(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t n, int64_t pitch,
-                   int64_t mat_pitch, uint32_t box_rows);
+                   int64_t mat_pitch, uint32_t box_cols, uint32_t box_rows);
 
 // Programmatic dependent launch. A kernel launched with launch_dependent may start while the one
 // before it in the stream still runs, from the moment all of that one's blocks have called

@@ -45,15 +45,10 @@ enum OrthKind { kGram = 0, kSquare = 1, kUpdate = 2 };
 
 struct OrthArgs {
     int n, p, rows, cols;
-    int64_t x_pitch, x_mat;  // X buffers: row and matrix pitch in elements
-    int64_t a_pitch, a_mat;  // A and B
-    int64_t r_mat;           // diagonal remainders: floats per matrix
-    const __half *xh;        // X, hi (the GEMM operand)
-    __half *xh_out;          // next X, hi
-    __half *xl;              // X, lo: updated in place
-    __half *ah, *al, *bh;
-    float *ra, *rb;
+    int64_t r_mat;           // floats per matrix of ra and rb
+    float *ra, *rb;          // diagonal remainders of A and B
     __nv_bfloat16 *out;      // [n, rows, cols], the last update's destination (else NULL)
+    int out_wide;            // rows of out are 16-byte aligned: they leave by TMA
     float a, b, c, out_scale;
 };
 
@@ -120,6 +115,7 @@ __global__ void __launch_bounds__(256)
     orth_norm_kernel(const PrepArgs a)
 {
     __shared__ double warp_sum[8];
+    allow_dependents();
     const int64_t elems = static_cast<int64_t>(a.rows) * a.cols;
     const int64_t base = blockIdx.y * elems;
     const G *g = static_cast<const G *>(a.grad) + base;
@@ -177,6 +173,8 @@ __global__ void __launch_bounds__(256)
     orth_cast_kernel(const PrepArgs a)
 {
     __shared__ double inv_s;
+    allow_dependents();
+    dependency_wait();
     if (threadIdx.x == 0) {
         double s = 0.0;
         for (int i = 0; i < a.parts; ++i)
@@ -227,22 +225,40 @@ __global__ void __launch_bounds__(256)
 }
 
 // -------------------------------------------------------------------------------- products
-// One persistent kernel per product, one CTA per SM: warp 0 TMA producer, warp 1 MMA issuer and
-// TMEM owner, warps 2.. epilogue. A tile is 128 rows x 128 columns of one matrix; two
-// accumulators in TMEM let a tile's epilogue overlap the next tile's K loop. An operand is K-major
-// (X rows in A = X X^T) or MN-major (X columns in X^T X and B X), as the layout gives it: X is never
-// transposed. Symmetric products compute the tiles on and above the diagonal and store each
-// tile also mirrored.
-constexpr int kBM = 128, kBN = 128;
-constexpr int kStages = 6;
-constexpr uint32_t kOperand = 16384;  // 128 x 64 fp16
-constexpr uint32_t kStageBytes = 2 * kOperand;
-constexpr int kEpiWarps = 4;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr uint32_t kBarOff = kStages * kStageBytes;
-constexpr uint32_t kMiscOff = kBarOff + 8 * (2 * kStages + 5);
-constexpr uint32_t kSmem = kMiscOff + 16 + 1024;
-static_assert(kSmem <= static_cast<uint32_t>(kMaxDynSmem), "ring exceeds shared memory");
+// One persistent kernel per product: warp 0 TMA producer, warp 1 MMA issuer and TMEM owner, warp 2
+// the epilogue's mover, warps 3.. the epilogue; two accumulators in TMEM let a tile's epilogue overlap the next tile's K loop. An
+// operand is K-major (X rows in A = X X^T) or MN-major (X columns in X^T X and B X), as the layout
+// gives it: X is never transposed. Symmetric products compute the tiles on and above the diagonal
+// and store each tile also mirrored.
+//
+// Two shapes. CTA pairs (cta_group::2): tiles of 256 x 256, each CTA holding 128 rows of A and of B
+// and its 128 rows of the result, so an MMA reads half as much shared memory per flop. Single CTAs:
+// tiles of 128 x 128, for matrices that 256-wide tiles would fill badly.
+//
+// The epilogue works on blocks of 128 rows x 32 columns in a ring of kBlocks buffers: a mover thread
+// brings a block's old hi and lo in by TMA, one of four groups of four warps replaces them in place,
+// each thread its part of one row, and the mover stores them and refills the buffer, up to kBlocks
+// blocks ahead and across tiles. The update's K loop is short (p), and its epilogue bounds it: the 36 x
+// 4096 x 1280 update took 554 us with one row per thread straight from and to global memory (32 lines
+// an access), 475 us with a buffer per group that it refilled itself, 456 us so; 297 us without
+// any epilogue, 365 us without its stores, 382 us without its arithmetic.
+template <bool PAIR>
+struct OrthGeo {
+    static constexpr int kTile = PAIR ? 256 : 128;     // rows and columns of a tile
+    static constexpr int kStages = 4;                  // 64-wide K slices in flight
+    static constexpr int kGroups = 4;                  // epilogue groups of four warps
+    static constexpr int kBlocks = 6;                  // epilogue buffers
+    static constexpr int kThreads = 96 + 128 * kGroups;
+    static constexpr uint32_t kOperand = 16384;        // 128 x 64 fp16: an operand's K slice
+    static constexpr uint32_t kBlock = 8192;           // 128 x 32 fp16: a block's hi or lo
+    static constexpr uint32_t kStageBytes = 2 * kOperand;
+    static constexpr uint32_t kEpiOff = kStages * kStageBytes;
+    static constexpr uint32_t kBarOff = kEpiOff + kBlocks * 2 * kBlock;
+    static constexpr uint32_t kMiscOff = kBarOff + 8 * (2 * kStages + 5 + 2 * kBlocks);
+    static constexpr uint32_t kSmem = kMiscOff + 16 + 1024;
+    static constexpr uint32_t kTmemCols = 2 * kTile;
+    static_assert(kSmem <= static_cast<uint32_t>(kMaxDynSmem), "ring exceeds shared memory");
+};
 
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N)
 {
@@ -261,19 +277,28 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr)
     return d;
 }
 
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, uint64_t *bar, int32_t c0, int32_t c1,
+// One box into this CTA's shared memory; the bytes count on `bar`, a shared::cluster address (on CTA
+// pairs the leader's barrier).
+template <bool PAIR>
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, uint32_t bar, int32_t c0, int32_t c1,
                                             int32_t c2)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
-        "[%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
+    if (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+            "{%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+            "[%2];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
 }
 
 struct OrthTile {
-    int mat, m0, n0;
-    bool mirror;  // a symmetric product's tile above the diagonal
+    int mat, ti, tj;  // matrix, block row and block column of the result
 };
 
 // Tiles of one matrix: the triangle ti <= tj of nm x nm, or nm x nn.
@@ -289,293 +314,490 @@ __device__ __forceinline__ OrthTile tile_at(int tile, int per, int nm, int nn)
     OrthTile t;
     t.mat = tile / per;
     const int u = tile - t.mat * per;
-    int ti, tj;
     if (KIND == kUpdate) {
-        ti = u / nn;
-        tj = u - ti * nn;
+        t.ti = u / nn;
+        t.tj = u - t.ti * nn;
     } else {
-        // row ti of the triangle starts at ti * nm - ti (ti - 1) / 2
-        ti = 0;
-        int first = 0;
-        while (first + nm - ti <= u) {
-            first += nm - ti;
-            ++ti;
+        int first = 0;  // first tile of block row ti
+        t.ti = 0;
+        while (first + nm - t.ti <= u) {
+            first += nm - t.ti;
+            ++t.ti;
         }
-        tj = ti + (u - first);
+        t.tj = t.ti + (u - first);
     }
-    t.m0 = ti * kBM;
-    t.n0 = tj * kBN;
-    t.mirror = KIND != kUpdate && tj > ti;
     return t;
 }
 
-// Eight columns [col, col + 8) of a row as floats (hi + lo).
-__device__ __forceinline__ void load_pair8(const __half *hi, const __half *lo, int64_t at, float (&v)[8])
+// The maps of the epilogue's blocks (32 columns x 128 rows, 64-byte swizzle): old hi and lo in, new hi and lo out.
+struct EpiMaps {
+    CUtensorMap in_hi, in_lo, out_hi, out_lo;
+};
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, const void *src, int32_t c0, int32_t c1, int32_t c2)
 {
-    const uint4 h = *reinterpret_cast<const uint4 *>(hi + at), l = *reinterpret_cast<const uint4 *>(lo + at);
-    const __half2 *hp = reinterpret_cast<const __half2 *>(&h), *lp = reinterpret_cast<const __half2 *>(&l);
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
+__device__ __forceinline__ float2 join_f16(uint32_t hi, uint32_t lo)
+{
+    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    return make_float2(fmaf(l.x, 1.0f / kLo, h.x), fmaf(l.y, 1.0f / kLo, h.y));
+}
+
+// hi and lo parts of two values: hi = fp16(v), lo = fp16((v - hi) kLo), both exact but for their last rounding.
+__device__ __forceinline__ float2 split_pair(float v0, float v1, uint32_t &hi, uint32_t &lo)
+{
+    const __half2 h = __floats2half2_rn(v0, v1);
+    const float2 f = __half22float2(h);
+    const float2 rest = make_float2(v0 - f.x, v1 - f.y);
+    const __half2 l = __floats2half2_rn(rest.x * kLo, rest.y * kLo);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+    return rest;
+}
+
+// 16 columns [col0, col0 + 16) of row `row`, which is row r and 16-byte chunks 2 * part .. of the staged
+// block (64-byte swizzle). Columns from N on and rows from M on are cut off by the stores.
+template <int KIND, bool TALL>
+__device__ __forceinline__ void epi_part(const OrthArgs &a, int mat, int row, int col0, int M, int N,
+                                         const float (&acc)[16], uint8_t *hi, uint8_t *lo, int r, int part)
+{
+    const float *rd = (KIND == kUpdate ? a.rb : a.ra) + mat * a.r_mat;  // padded to a multiple of 64
+    constexpr bool per_row = KIND == kSquare || (KIND == kUpdate && !TALL);
+    constexpr bool per_col = KIND == kSquare || (KIND == kUpdate && TALL);
+    const float r_row = per_row && row < M ? rd[row] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 a = __half22float2(hp[i]), b = __half22float2(lp[i]);
-        v[2 * i] = fmaf(b.x, 1.0f / kLo, a.x);
-        v[2 * i + 1] = fmaf(b.y, 1.0f / kLo, a.y);
+    for (int c = 0; c < 2; ++c) {
+        const uint32_t at = r * 64 + (((part * 2 + c) ^ ((r >> 1) & 3)) << 4);
+        uint4 h4 = make_uint4(0, 0, 0, 0), l4 = make_uint4(0, 0, 0, 0);
+        if (KIND != kGram) {
+            h4 = *reinterpret_cast<const uint4 *>(hi + at);
+            l4 = *reinterpret_cast<const uint4 *>(lo + at);
+        }
+        uint32_t h[4] = {h4.x, h4.y, h4.z, h4.w}, l[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int col = col0 + 8 * c + 2 * i;
+            const float m0 = acc[8 * c + 2 * i], m1 = acc[8 * c + 2 * i + 1];
+            float v0, v1;
+            if (KIND == kGram) {
+                v0 = m0 * (kSa / (kSx * kSx));
+                v1 = m1 * (kSa / (kSx * kSx));
+            } else {
+                const float2 old = join_f16(h[i], l[i]);
+                float2 rr = make_float2(r_row, r_row);
+                if (per_col) {
+                    const float2 rc = *reinterpret_cast<const float2 *>(rd + col);
+                    rr.x += rc.x;
+                    rr.y += rc.y;
+                }
+                if (KIND == kSquare) {
+                    const float f = a.c * (kSb / kSa) * (1.0f / kSa);
+                    v0 = fmaf(a.b, old.x, f * fmaf(rr.x, old.x, m0));
+                    v1 = fmaf(a.b, old.y, f * fmaf(rr.y, old.y, m1));
+                } else {
+                    v0 = fmaf(fmaf(rr.x, 1.0f / kSb, a.a), old.x, m0 * (1.0f / kSb));
+                    v1 = fmaf(fmaf(rr.y, 1.0f / kSb, a.a), old.y, m1 * (1.0f / kSb));
+                }
+            }
+            if (KIND == kUpdate && a.out) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v0 * a.out_scale, v1 * a.out_scale);
+                h[i] = *reinterpret_cast<const uint32_t *>(&b);
+            } else {
+                const float2 rest = split_pair(v0, v1, h[i], l[i]);
+                if (KIND != kUpdate && row - col >= 0 && row - col < 2 && row < M)  // the diagonal
+                    ((KIND == kGram) ? a.ra : a.rb)[mat * a.r_mat + row] = row == col ? rest.x : rest.y;
+            }
+        }
+        if (KIND == kUpdate && a.out && !a.out_wide) {
+            __nv_bfloat16 *o = a.out + (static_cast<int64_t>(mat) * a.rows + row) * a.cols + col0 + 8 * c;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (row < M && col0 + 8 * c + i < N)
+                    o[i] = __ushort_as_bfloat16(static_cast<uint16_t>(h[i / 2] >> (i % 2 * 16)));
+            continue;
+        }
+        *reinterpret_cast<uint4 *>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (KIND == kGram || (KIND == kUpdate && !a.out))
+            *reinterpret_cast<uint4 *>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
     }
 }
 
-// Epilogue of 32 columns [col0, col0 + 32) of this thread's row of a tile.
-template <int KIND, bool TALL>
-__device__ __forceinline__ void orth_epilogue(const OrthArgs &a, const OrthTile &t, int row, int col0,
-                                              const float (&acc)[32])
+// An operand from a symmetric matrix of which only the blocks on and above the diagonal are
+// stored: rows of block row `blk`, K slice k0. Block (blk, k0 / TILE) is stored if it is not below
+// the diagonal (K-major boxes); else its mirror image is, and is read as an MN-major operand.
+template <int TILE>
+__device__ __forceinline__ bool stored_mirrored(int blk, int k0)
 {
-    const int M = KIND == kUpdate ? a.rows : a.p, N = KIND == kUpdate ? a.cols : a.p;
-    if (row >= M)
-        return;
-    if (KIND == kUpdate) {
-        const int64_t base = t.mat * a.x_mat + row * a.x_pitch;
-        const float *rb = a.rb + t.mat * a.r_mat;
-        const float row_r = TALL ? 0.0f : a.a + rb[row] * (1.0f / kSb);
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int col = col0 + 8 * g;
-            if (col >= N)
-                break;
-            float x[8];
-            load_pair8(a.xh, a.xl, base + col, x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float f = TALL ? a.a + (col + i < N ? rb[col + i] : 0.0f) * (1.0f / kSb) : row_r;
-                x[i] = fmaf(f, x[i], acc[8 * g + i] * (1.0f / kSb));
-            }
-            if (a.out) {
-                const int64_t o = (static_cast<int64_t>(t.mat) * a.rows + row) * a.cols + col;
-                alignas(16) __nv_bfloat16 v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] = __float2bfloat16_rn(x[i] * a.out_scale);
-                if (a.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0) {
-                    *reinterpret_cast<uint4 *>(a.out + o) = *reinterpret_cast<const uint4 *>(v);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (col + i < N)
-                            a.out[o + i] = v[i];
-                }
-            } else {
-                alignas(16) __half hi[8], lo[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    split_f16(x[i], hi[i], lo[i]);
-                *reinterpret_cast<uint4 *>(a.xh_out + base + col) = *reinterpret_cast<const uint4 *>(hi);
-                *reinterpret_cast<uint4 *>(a.xl + base + col) = *reinterpret_cast<const uint4 *>(lo);
-            }
-        }
-        return;
-    }
-    const int64_t mat = t.mat * a.a_mat;
-    const int64_t base = mat + row * a.a_pitch;
-    const float *ra = a.ra + t.mat * a.r_mat;
-    const float ra_row = KIND == kSquare ? ra[row] : 0.0f;
-    __half *dst = KIND == kGram ? a.ah : a.bh;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int col = col0 + 8 * g;
-        if (col >= N)
-            break;
-        float v[8];
-        if (KIND == kGram) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = acc[8 * g + i] * (kSa / (kSx * kSx));
-        } else {
-            float x[8];
-            load_pair8(a.ah, a.al, base + col, x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float r = ra_row + (col + i < N ? ra[col + i] : 0.0f);
-                v[i] = fmaf(a.b, x[i], a.c * (kSb / kSa) * (fmaf(r, x[i], acc[8 * g + i]) * (1.0f / kSa)));
-            }
-        }
-        alignas(16) __half hi[8], lo[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            split_f16(v[i], hi[i], lo[i]);
-            if (col + i == row)
-                (KIND == kGram ? a.ra : a.rb)[t.mat * a.r_mat + row] = v[i] - __half2float(hi[i]);
-        }
-        *reinterpret_cast<uint4 *>(dst + base + col) = *reinterpret_cast<const uint4 *>(hi);
-        if (KIND == kGram)
-            *reinterpret_cast<uint4 *>(a.al + base + col) = *reinterpret_cast<const uint4 *>(lo);
-        if (t.mirror)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (col + i < N)
-                    dst[mat + (col + i) * a.a_pitch + row] = hi[i];
+    return k0 / TILE < blk;
+}
+
+// 128 rows (from mn0) x 64 (from k0) of an operand into shared memory.
+template <bool PAIR>
+__device__ __forceinline__ void load_operand(uint8_t *dst, const CUtensorMap *km, const CUtensorMap *mn, uint32_t bar,
+                                             int mn0, int k0, int mat, bool mn_major)
+{
+    if (mn_major) {
+        tma_load_3d<PAIR>(dst, mn, bar, mn0, k0, mat);
+        tma_load_3d<PAIR>(dst + 8192, mn, bar, mn0 + 64, k0, mat);
+    } else {
+        tma_load_3d<PAIR>(dst, km, bar, k0, mn0, mat);
     }
 }
+
+// The epilogue's blocks of one CTA in order: the 32-column blocks of its tiles. A pair's second half of
+// a tile that lies outside the matrix has none.
+template <int KIND, int TILE>
+struct BlockWalk {
+    int tile, b, nb, row0, n0;
+    OrthTile t;
+    __device__ __forceinline__ void start(int first, int tiles, int stride, int per, int nm, int nn, int rank, int M, int N)
+    {
+        tile = first - stride;
+        b = nb = 0;
+        next(tiles, stride, per, nm, nn, rank, M, N);
+    }
+    // to the next block (b = nb = 0 on entry: to the first block of the tile after `tile`)
+    __device__ __forceinline__ void next(int tiles, int stride, int per, int nm, int nn, int rank, int M, int N)
+    {
+        if (++b < nb)
+            return;
+        do {
+            tile += stride;
+            if (tile >= tiles)
+                return;
+            t = tile_at<KIND>(tile, per, nm, nn);
+            row0 = t.ti * TILE + rank * 128;
+            n0 = t.tj * TILE;
+            nb = row0 < M ? ((N - n0 < TILE ? N - n0 : TILE) + 31) / 32 : 0;
+        } while (nb == 0);
+        b = 0;
+    }
+};
 
 // MN-major operands: X in A = X^T X (tall) and the right factor X of B X (wide).
-template <int KIND, bool TALL>
-__global__ void __launch_bounds__(kThreads, 1)
-    orth_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                     const OrthArgs a, const WaitCfg wc)
+//
+// On CTA pairs the leader (cluster rank 0) issues the MMAs; both CTAs' loads count on the leader's
+// full barriers, the leader's commits arrive in both CTAs, and both epilogues arrive on the leader's
+// accumulator-empty barriers.
+template <int KIND, bool TALL, bool PAIR>
+__global__ void __launch_bounds__(OrthGeo<PAIR>::kThreads, 1)
+    orth_gemm_kernel(const __grid_constant__ CUtensorMap a_km, const __grid_constant__ CUtensorMap a_mn,
+                     const __grid_constant__ CUtensorMap b_km, const __grid_constant__ CUtensorMap b_mn,
+                     const __grid_constant__ EpiMaps em, const OrthArgs a, const WaitCfg wc)
 {
+    using G = OrthGeo<PAIR>;
+    constexpr int S = G::kStages, TILE = G::kTile;
+    // operand sources: a symmetric matrix (A, B), or X as its layout gives it
+    constexpr bool kAsym = KIND == kSquare || (KIND == kUpdate && !TALL);
+    constexpr bool kBsym = KIND == kSquare || (KIND == kUpdate && TALL);
     constexpr bool kAmn = KIND == kGram && TALL;
     constexpr bool kBmn = (KIND == kGram && TALL) || (KIND == kUpdate && !TALL);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kBarOff);
-    uint64_t *empty = full + kStages;
-    uint64_t *accf = empty + kStages;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + G::kBarOff);
+    uint64_t *empty = full + S;
+    uint64_t *accf = empty + S;
     uint64_t *acce = accf + 2;
     uint64_t *drain = acce + 2;
-    uint32_t *holder = reinterpret_cast<uint32_t *>(smem + kMiscOff);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kMiscOff + 4);
+    uint64_t *bfull = drain + 1;           // [kBlocks] a block's old values have landed
+    uint64_t *bdone = bfull + G::kBlocks;  // [kBlocks] its new ones are written
+    uint32_t *holder = reinterpret_cast<uint32_t *>(smem + G::kMiscOff);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + G::kMiscOff + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+    const uint32_t full0 = PAIR ? dsmem_addr(smem_u32(full), 0) : smem_u32(full);
+    const uint32_t acce0 = PAIR ? dsmem_addr(smem_u32(acce), 0) : smem_u32(acce);
+    allow_dependents();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accf[b], 1);
-            mbar_init(&acce[b], kEpiWarps);
+            mbar_init(&acce[b], (PAIR ? 2 : 1) * 4 * G::kGroups);
+        }
+        for (int b = 0; b < G::kBlocks; ++b) {
+            mbar_init(&bfull[b], 1);
+            mbar_init(&bdone[b], 4);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
+        tma_prefetch_map(&a_km);
+        tma_prefetch_map(&a_mn);
+        tma_prefetch_map(&b_km);
+        tma_prefetch_map(&b_mn);
     }
     if (warp == 1) {
-        tmem_alloc(holder, 2 * kBN);
-        tmem_relinquish();
+        if (PAIR) {
+            tmem_alloc_pair(holder, G::kTmemCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(holder, G::kTmemCols);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
-    __syncthreads();
+    if (PAIR)
+        cluster_sync_all();  // both CTAs' barriers are initialised before any remote arrival
+    else
+        __syncthreads();
     tc_fence_after();
+    dependency_wait();  // the launch before has written this one's operands
     const uint32_t tmem = *holder;
     const int M = KIND == kUpdate ? a.rows : a.p, N = KIND == kUpdate ? a.cols : a.p;
     const int K = KIND == kGram ? (TALL ? a.rows : a.cols) : a.p;
-    const int nm = (M + kBM - 1) / kBM, nn = (N + kBN - 1) / kBN;
-    const int nk = (K + 63) / 64;
+    const int nm = (M + TILE - 1) / TILE, nn = (N + TILE - 1) / TILE;
+    const int nk = (K + 63) / 64;  // K slices of a tile
     const int per = tiles_of<KIND>(nm, nn);
     const int tiles = per * a.n;
+    const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, stride = PAIR ? gridDim.x >> 1 : gridDim.x;
 
     if (warp == 0) {
         if (lane == 0) {
-            tma_prefetch_map(&tm_a);
-            tma_prefetch_map(&tm_b);
             int it = 0;
             bool stop = false;
-            for (int tile = blockIdx.x; tile < tiles && !stop; tile += gridDim.x) {
+            for (int tile = first; tile < tiles && !stop; tile += stride) {
                 const OrthTile t = tile_at<KIND>(tile, per, nm, nn);
+                const int m0 = t.ti * TILE + rank * 128, n0 = t.tj * TILE + rank * 128;
                 for (int kb = 0; kb < nk; ++kb, ++it) {
-                    const int s = it % kStages;
-                    if (!mbar_wait(&empty[s], ((it / kStages) & 1) ^ 1, wc, abort_flag)) {
+                    const int s = it % S;
+                    if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1, wc, abort_flag)) {
                         stop = true;
                         break;
                     }
-                    mbar_arrive_expect_tx(&full[s], kStageBytes);
-                    uint8_t *A = smem + s * kStageBytes, *B = A + kOperand;
-                    if (kAmn) {
-                        tma_load_3d(A, &tm_a, &full[s], t.m0, kb * 64, t.mat);
-                        tma_load_3d(A + 8192, &tm_a, &full[s], t.m0 + 64, kb * 64, t.mat);
-                    } else {
-                        tma_load_3d(A, &tm_a, &full[s], kb * 64, t.m0, t.mat);
-                    }
-                    if (kBmn) {
-                        tma_load_3d(B, &tm_b, &full[s], t.n0, kb * 64, t.mat);
-                        tma_load_3d(B + 8192, &tm_b, &full[s], t.n0 + 64, kb * 64, t.mat);
-                    } else {
-                        tma_load_3d(B, &tm_b, &full[s], kb * 64, t.n0, t.mat);
-                    }
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * G::kStageBytes);
+                    uint8_t *A = smem + s * G::kStageBytes, *B = A + G::kOperand;
+                    const uint32_t bar = full0 + 8 * s;
+                    const int k0 = kb * 64;
+                    load_operand<PAIR>(A, &a_km, &a_mn, bar, m0, k0, t.mat,
+                                       kAsym ? stored_mirrored<TILE>(t.ti, k0) : kAmn);
+                    load_operand<PAIR>(B, &b_km, &b_mn, bar, n0, k0, t.mat,
+                                       kBsym ? stored_mirrored<TILE>(t.tj, k0) : kBmn);
                 }
             }
-            for (int i = it > kStages ? it - kStages : 0; i < it; ++i)
-                mbar_wait_drain(&full[i % kStages], (i / kStages) & 1, wc);
+            // The loads this CTA issued must have landed before it leaves. The leader's barriers
+            // count both CTAs' bytes; the peer, which cannot wait on them, leaves behind the final
+            // cluster barrier, and after an abort (when it may have issued stages that the leader never
+            // armed) waits 200 us first, far longer than a load takes.
+            if (rank == 0) {
+                for (int i = it > S ? it - S : 0; i < it; ++i)
+                    mbar_wait_drain(&full[i % S], (i / S) & 1, wc);
+            } else if (stop || *abort_flag) {
+                const unsigned long long t0 = global_ns();
+                while (global_ns() - t0 < 200000ull) {
+                }
+            }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int it = 0, tc = 0;
+        if (lane == 0 && rank == 0) {
+            int tc = 0, s = 0;
+            uint32_t par = 0;
             bool ok = true;
-            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++tc) {
+            for (int tile = first; tile < tiles && ok; tile += stride, ++tc) {
                 const OrthTile t = tile_at<KIND>(tile, per, nm, nn);
                 const int buf = tc & 1;
                 if (!mbar_wait(&acce[buf], ((tc >> 1) & 1) ^ 1, wc, abort_flag))
                     break;
                 tc_fence_after();
-                const int left = N - t.n0;
-                const int cols = left < kBN ? (left + 15) & ~15 : kBN;
-                const uint32_t idesc = idesc_f16_f32(kBM, cols) | (kAmn ? 1u << 15 : 0u) | (kBmn ? 1u << 16 : 0u);
-                for (int kb = 0; kb < nk; ++kb, ++it) {
-                    const int s = it % kStages;
-                    if (!mbar_wait(&full[s], (it / kStages) & 1, wc, abort_flag)) {
+                const int left = N - t.tj * TILE;
+                const int cols = !PAIR && left < TILE ? (left + 15) & ~15 : TILE;
+                const uint32_t d = tmem + buf * TILE;
+                bool ready = mbar_test(&full[s], par);
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!ready && !mbar_wait(&full[s], par, wc, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kOperand;
+                    const int cur = s;
+                    if (++s == S) {
+                        s = 0;
+                        par ^= 1;
+                    }
+                    // the next slice's barrier is asked for ahead of this slice's MMAs: its answer comes
+                    // while they are issued, and the pipe does not run dry for the length of a test
+                    ready = mbar_test(&full[s], par);
+                    const uint32_t sa = smem_u32(smem + cur * G::kStageBytes), sb = sa + G::kOperand;
+                    const bool amn = kAsym ? stored_mirrored<TILE>(t.ti, kb * 64) : kAmn;
+                    const bool bmn = kBsym ? stored_mirrored<TILE>(t.tj, kb * 64) : kBmn;
+                    // one K step of 16: 32 bytes of a K-major row, 16 rows of an MN-major operand
+                    const uint64_t ad = amn ? sdesc_mn(sa) : sdesc_kmajor_sw128(sa);
+                    const uint64_t bd = bmn ? sdesc_mn(sb) : sdesc_kmajor_sw128(sb);
+                    const int as = amn ? 2048 >> 4 : 2, bs = bmn ? 2048 >> 4 : 2;
+                    const uint32_t idesc =
+                        idesc_f16_f32(TILE, cols) | (amn ? 1u << 15 : 0u) | (bmn ? 1u << 16 : 0u);
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
-                        const uint64_t ad = kAmn ? sdesc_mn(sa + ks * 2048) : sdesc_kmajor_sw128(sa) + 2 * ks;
-                        const uint64_t bd = kBmn ? sdesc_mn(sb + ks * 2048) : sdesc_kmajor_sw128(sb) + 2 * ks;
-                        umma_bf16(tmem + buf * kBN, ad, bd, idesc, (kb | ks) != 0);  // kind::f16: fp16 by idesc
+                        // kind::f16: the operands' type, fp16, is in idesc
+                        if (PAIR)
+                            umma_bf16_pair(d, ad + as * ks, bd + bs * ks, idesc, (kb | ks) != 0);
+                        else
+                            umma_bf16(d, ad + as * ks, bd + bs * ks, idesc, (kb | ks) != 0);
                     }
-                    umma_commit(&empty[s]);
+                    if (PAIR)
+                        umma_commit_pair_mc(&empty[cur], 0x3);
+                    else
+                        umma_commit(&empty[cur]);
                 }
-                if (ok)
-                    umma_commit(&accf[buf]);
+                if (ok) {
+                    if (PAIR)
+                        umma_commit_pair_mc(&accf[buf], 0x3);
+                    else
+                        umma_commit(&accf[buf]);
+                }
             }
-            umma_commit(drain);
+            if (PAIR)
+                umma_commit_pair_mc(drain, 0x3);
+            else
+                umma_commit(drain);
+        }
+        if (lane == 0)
             mbar_wait_drain(drain, 0, wc);
+    } else if (warp == 2) {
+        if (lane == 0) {
+            const bool last = KIND == kUpdate && a.out != nullptr;
+            BlockWalk<KIND, TILE> in, out;
+            in.start(first, tiles, stride, per, nm, nn, rank, M, N);
+            out = in;
+            int loaded = 0;
+            const auto fetch = [&]() {
+                const int u = loaded % G::kBlocks;
+                uint8_t *hi = smem + G::kEpiOff + u * 2 * G::kBlock;
+                if (KIND == kGram) {
+                    mbar_arrive(&bfull[u]);
+                } else {
+                    mbar_arrive_expect_tx(&bfull[u], 2 * G::kBlock);
+                    tma_load_3d<false>(hi, &em.in_hi, smem_u32(&bfull[u]), in.n0 + in.b * 32, in.row0, in.t.mat);
+                    tma_load_3d<false>(hi + G::kBlock, &em.in_lo, smem_u32(&bfull[u]), in.n0 + in.b * 32, in.row0,
+                                       in.t.mat);
+                }
+                ++loaded;
+                in.next(tiles, stride, per, nm, nn, rank, M, N);
+            };
+            while (loaded < G::kBlocks && in.tile < tiles)
+                fetch();
+            for (int i = 0; out.tile < tiles; ++i) {
+                const int u = i % G::kBlocks;
+                if (!mbar_wait(&bdone[u], (i / G::kBlocks) & 1, wc, abort_flag))
+                    break;
+                const uint8_t *hi = smem + G::kEpiOff + u * 2 * G::kBlock;
+                if (!last || a.out_wide)
+                    tma_store_3d(&em.out_hi, hi, out.n0 + out.b * 32, out.row0, out.t.mat);
+                if (KIND == kGram || (KIND == kUpdate && !last))
+                    tma_store_3d(&em.out_lo, hi + G::kBlock, out.n0 + out.b * 32, out.row0, out.t.mat);
+                bulk_commit();
+                out.next(tiles, stride, per, nm, nn, rank, M, N);
+                if (in.tile < tiles) {
+                    bulk_wait_read<0>();
+                    fetch();
+                }
+            }
+            // every load has landed and every store arrived before the CTA (and its shared memory) goes
+            for (int i = loaded > G::kBlocks ? loaded - G::kBlocks : 0; i < loaded; ++i)
+                mbar_wait_drain(&bfull[i % G::kBlocks], (i / G::kBlocks) & 1, wc);
+            bulk_wait<0>();
         }
     } else {
-        const int q = warp & 3;
-        int tc = 0;
-        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++tc) {
+        const int q = warp & 3, grp = (warp - 3) / 4, r = q * 32 + lane;
+        int tc = 0, i0 = 0;  // i0: blocks of the CTA before the tile's
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += stride, ++tc) {
             const OrthTile t = tile_at<KIND>(tile, per, nm, nn);
             const int buf = tc & 1;
-            if (!warp_wait(&accf[buf], (tc >> 1) & 1, wc, abort_flag))
-                break;
+            const int row0 = t.ti * TILE + rank * 128, n0 = t.tj * TILE;
+            const int nb = row0 < M ? ((N - n0 < TILE ? N - n0 : TILE) + 31) / 32 : 0;
+            ok = warp_wait(&accf[buf], (tc >> 1) & 1, wc, abort_flag);
             tc_fence_after();
-            const int row = t.m0 + q * 32 + lane;
-            for (int cb = 0; cb < kBN && t.n0 + cb < N; cb += 32) {
-                float v[32];
-                tmem_load32(tmem + buf * kBN + (static_cast<uint32_t>(q * 32) << 16) + cb, v);
-                orth_epilogue<KIND, TALL>(a, t, row, t.n0 + cb, v);
+            for (int b = grp; b < nb && ok; b += G::kGroups) {
+                const int i = i0 + b, u = i % G::kBlocks;
+                ok = warp_wait(&bfull[u], (i / G::kBlocks) & 1, wc, abort_flag);
+                if (!ok)
+                    break;
+                uint8_t *hi = smem + G::kEpiOff + u * 2 * G::kBlock;
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    const int off = b * 32 + part * 16;
+                    float v[16];
+                    tmem_load16(tmem + buf * TILE + (static_cast<uint32_t>(q * 32) << 16) + off, v);
+                    epi_part<KIND, TALL>(a, t.mat, row0 + r, n0 + off, M, N, v, hi, hi + G::kBlock, r, part);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bdone[u]);
             }
+            i0 += nb;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&acce[buf]);
+            if (lane == 0 && ok) {
+                if (PAIR)
+                    mbar_arrive_cluster(acce0 + 8 * buf);
+                else
+                    mbar_arrive(&acce[buf]);
+            }
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if (PAIR)
+        cluster_sync_all();  // both CTAs are done with TMEM, shared memory and each other's barriers
+    else
+        __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 2 * kBN);
+        if (PAIR)
+            tmem_dealloc_pair(tmem, G::kTmemCols);
+        else
+            tmem_dealloc(tmem, G::kTmemCols);
     }
 }
 
-template <int KIND, bool TALL>
-cudaError_t launch_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const OrthArgs &a, const DeviceContext &dc,
+template <int KIND, bool TALL, bool PAIR>
+cudaError_t launch_gemm(const CUtensorMap &a_km, const CUtensorMap &a_mn, const CUtensorMap &b_km,
+                        const CUtensorMap &b_mn, const EpiMaps &em, const OrthArgs &a, const DeviceContext &dc,
                         cudaStream_t stream)
 {
-    const cudaError_t err = cudaFuncSetAttribute(orth_gemm_kernel<KIND, TALL>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    using G = OrthGeo<PAIR>;
+    auto kernel = orth_gemm_kernel<KIND, TALL, PAIR>;
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(G::kSmem));
     if (err != cudaSuccess)
         return err;
     const int M = KIND == kUpdate ? a.rows : a.p, N = KIND == kUpdate ? a.cols : a.p;
-    const int nm = (M + kBM - 1) / kBM, nn = (N + kBN - 1) / kBN;
+    const int nm = (M + G::kTile - 1) / G::kTile, nn = (N + G::kTile - 1) / G::kTile;
     const int64_t tiles = static_cast<int64_t>(KIND == kUpdate ? nm * nn : nm * (nm + 1) / 2) * a.n;
-    const int grid = static_cast<int>(tiles < dc.num_sms ? tiles : dc.num_sms);
-    orth_gemm_kernel<KIND, TALL><<<grid, kThreads, kSmem, stream>>>(ma, mb, a, dc.wait);
-    return cudaGetLastError();
+    const int64_t slots = PAIR ? dc.num_sms / 2 : dc.num_sms;
+    const int grid = static_cast<int>(tiles < slots ? tiles : slots) * (PAIR ? 2 : 1);
+    return launch_dependent(kernel, dim3(grid), G::kThreads, G::kSmem, stream, PAIR ? 2 : 1, a_km, a_mn,
+                            b_km, b_mn, em, a, dc.wait);
 }
 
 // ------------------------------------------------------------------------------------ host
 constexpr int kMaxSide = 16384;
 constexpr int kMaxSteps = 32;
 constexpr size_t kChunkBytes = size_t(2) << 30;  // matrices worked on together fill at most this
+
+// Whether a step is faster on CTA pairs: the waves of tiles of the three products, weighted by their
+// K, a 256 x 256 pair tile taking 1.4 times a 128 x 128 one. Measured, single / pairs (us): 16 x
+// 384 x 1536 228 / 284, 64 x 300 x 900 620 / 766, 64 x 256 x 1024 320 / 322, 16 x 768 x 2048 696 / 600, 12 x 1280 x
+// 4096 2139 / 1619.
+bool use_pairs(int64_t n, int64_t p, int64_t q, int num_sms)
+{
+    const auto cost = [&](int64_t tile, int64_t slots) {
+        const int64_t nm = (p + tile - 1) / tile, nq = (q + tile - 1) / tile;
+        const auto waves = [&](int64_t tiles) { return (tiles * n + slots - 1) / slots; };
+        return waves(nm * (nm + 1) / 2) * (q + p) + waves(nm * nq) * p;
+    };
+    return cost(128, num_sms) * 10 > cost(256, num_sms / 2) * 14;
+}
 
 size_t up(size_t v, size_t to)
 {
@@ -681,59 +903,57 @@ cudaError_t launch_prep(const PrepArgs &a, int n, cudaStream_t stream)
         return err;
     const int64_t work = ((a.cols + 7) / 8 * static_cast<int64_t>(a.rows) + 255) / 256;
     const dim3 cgrid(static_cast<unsigned>(work < 512 ? work : 512), n);
-    if (a.cols % 8 == 0 && at % 16 == 0)
-        orth_cast_kernel<G, true><<<cgrid, 256, 0, stream>>>(a);
-    else
-        orth_cast_kernel<G, false><<<cgrid, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(a.cols % 8 == 0 && at % 16 == 0 ? orth_cast_kernel<G, true> : orth_cast_kernel<G, false>,
+                            cgrid, 256, 0, stream, 1, a);
 }
 
-template <bool TALL>
+template <bool TALL, bool PAIR>
 moe_status_t run_steps(const moe_orthogonalize_desc &d, const OrthLayout &L, const DeviceContext &dc, int n, uint8_t *w,
                        __nv_bfloat16 *out, cudaStream_t s)
 {
-    __half *xh[2] = {reinterpret_cast<__half *>(w + L.xh0), reinterpret_cast<__half *>(w + L.xh1)};
     OrthArgs a{};
     a.n = n;
     a.p = L.p;
     a.rows = d.rows;
     a.cols = d.cols;
-    a.x_pitch = L.x_pitch;
-    a.x_mat = L.x_mat;
-    a.a_pitch = L.a_pitch;
-    a.a_mat = L.a_mat;
     a.r_mat = L.r_mat;
-    a.xl = reinterpret_cast<__half *>(w + L.xl);
-    a.ah = reinterpret_cast<__half *>(w + L.ah);
-    a.al = reinterpret_cast<__half *>(w + L.al);
-    a.bh = reinterpret_cast<__half *>(w + L.bh);
     a.ra = reinterpret_cast<float *>(w + L.ra);
     a.rb = reinterpret_cast<float *>(w + L.rb);
     a.a = d.a;
     a.b = d.b;
     a.c = d.c;
     a.out_scale = d.scale / kSx;
-    CUtensorMap mk[2], mm[2], am, bm;  // X with K-major boxes (tall update, wide gram) and MN-major ones
-    bool ok = map_stack_f16(&am, a.ah, L.p, L.p, n, L.a_pitch, L.a_mat, 128) &&
-              map_stack_f16(&bm, a.bh, L.p, L.p, n, L.a_pitch, L.a_mat, 128);
-    for (int i = 0; i < 2 && ok; ++i)
-        ok = map_stack_f16(&mk[i], xh[i], d.cols, d.rows, n, L.x_pitch, L.x_mat, 128) &&
-             map_stack_f16(&mm[i], xh[i], d.cols, d.rows, n, L.x_pitch, L.x_mat, 64);
+    a.out_wide = d.cols % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
+    // each matrix with K-major boxes, with MN-major ones and with the epilogue's
+    const auto sym = [&](CUtensorMap *m, size_t off, uint32_t cols, uint32_t rows) {
+        return map_stack_f16(m, w + off, L.p, L.p, n, L.a_pitch, L.a_mat, cols, rows);
+    };
+    const auto xs = [&](CUtensorMap *m, size_t off, uint32_t cols, uint32_t rows) {
+        return map_stack_f16(m, w + off, d.cols, d.rows, n, L.x_pitch, L.x_mat, cols, rows);
+    };
+    const size_t xh[2] = {L.xh0, L.xh1};
+    CUtensorMap xk[2], xm[2], xe[2], xl, ak, am, ae, al, bk, bm, be, oe;
+    bool ok = sym(&ak, L.ah, 64, 128) && sym(&am, L.ah, 64, 64) && sym(&ae, L.ah, 32, 128) &&
+              sym(&al, L.al, 32, 128) && sym(&bk, L.bh, 64, 128) && sym(&bm, L.bh, 64, 64) &&
+              sym(&be, L.bh, 32, 128) && xs(&xl, L.xl, 32, 128);
+    for (int i = 0; i < 2; ++i)
+        ok = ok && xs(&xk[i], xh[i], 64, 128) && xs(&xm[i], xh[i], 64, 64) && xs(&xe[i], xh[i], 32, 128);
+    oe = xl;  // unused unless out_wide (to a copy bf16 and fp16 are the same 16 bits)
+    if (a.out_wide)
+        ok = ok && map_stack_f16(&oe, out, d.cols, d.rows, n, d.cols, static_cast<int64_t>(d.rows) * d.cols, 32, 128);
     if (!ok)
         return MOE_ERR_CUDA;
     cudaError_t e = cudaSuccess;
     for (int step = 0; step < d.steps && e == cudaSuccess; ++step) {
         const int cur = step & 1;
-        a.xh = xh[cur];
-        a.xh_out = xh[cur ^ 1];
         a.out = step + 1 == d.steps ? out : nullptr;
-        const CUtensorMap &gx = TALL ? mm[cur] : mk[cur];
-        e = launch_gemm<kGram, TALL>(gx, gx, a, dc, s);
+        e = launch_gemm<kGram, TALL, PAIR>(xk[cur], xm[cur], xk[cur], xm[cur], EpiMaps{ae, al, ae, al}, a, dc, s);
         if (e == cudaSuccess)
-            e = launch_gemm<kSquare, TALL>(am, am, a, dc, s);
+            e = launch_gemm<kSquare, TALL, PAIR>(ak, am, ak, am, EpiMaps{ae, al, be, be}, a, dc, s);
+        const EpiMaps em{xe[cur], xl, a.out ? oe : xe[cur ^ 1], xl};
         if (e == cudaSuccess)
-            e = TALL ? launch_gemm<kUpdate, TALL>(mk[cur], bm, a, dc, s)
-                     : launch_gemm<kUpdate, TALL>(bm, mm[cur], a, dc, s);
+            e = TALL ? launch_gemm<kUpdate, TALL, PAIR>(xk[cur], xm[cur], bk, bm, em, a, dc, s)
+                     : launch_gemm<kUpdate, TALL, PAIR>(bk, bm, xk[cur], xm[cur], em, a, dc, s);
     }
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -801,7 +1021,11 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc *desc, const void *g
         if (e != cudaSuccess)
             return MOE_ERR_CUDA;
         __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(out) + first * elems;
-        st = d.rows > d.cols ? run_steps<true>(d, L, dc, n, w, o, s) : run_steps<false>(d, L, dc, n, w, o, s);
+        const bool pair = use_pairs(n, L.p, d.rows < d.cols ? d.cols : d.rows, dc.num_sms);
+        st = d.rows > d.cols ? (pair ? run_steps<true, true>(d, L, dc, n, w, o, s)
+                                     : run_steps<true, false>(d, L, dc, n, w, o, s))
+                             : (pair ? run_steps<false, true>(d, L, dc, n, w, o, s)
+                                     : run_steps<false, false>(d, L, dc, n, w, o, s));
         if (st != MOE_OK)
             return st;
     }
