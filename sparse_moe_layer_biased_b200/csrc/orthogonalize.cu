@@ -101,12 +101,74 @@ __device__ __forceinline__ void load_gv(const __nv_bfloat16 *p, int64_t i, float
                 v[k + 2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
             }
         }
+    } else if (V == 4) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p + i);
+        v[0] = __uint_as_float(u.x << 16);
+        v[1 % V] = __uint_as_float(u.x & 0xffff0000u);
+        v[2 % V] = __uint_as_float(u.y << 16);
+        v[3 % V] = __uint_as_float(u.y & 0xffff0000u);
     } else {
 #pragma unroll
         for (int k = 0; k < V; ++k)
             v[k] = __bfloat162float(p[i + k]);
     }
 }
+
+// Sum of squares in fp32 whatever the elements' size: large, small and ordinary ones have sums of their
+// own, scaled so that no square leaves the range (Blue's three accumulators, 1978); 64-bit conversions
+// run at a quarter of a warp a cycle and would bound the kernels.
+struct Squares {
+    float big = 0.0f, mid = 0.0f, small = 0.0f;
+    __device__ __forceinline__ void add(float u)
+    {
+        const float m = fabsf(u);
+        if (m > 0x1p50f) {
+            const float v = u * 0x1p-70f;
+            big = fmaf(v, v, big);
+        } else if (m < 0x1p-50f) {
+            const float v = u * 0x1p90f;
+            small = fmaf(v, v, small);
+        } else {
+            mid = fmaf(u, u, mid);  // a NaN too
+        }
+    }
+    // Several at once: their plain sum of squares, if it is an ordinary number, else one by one. (What
+    // underflows beside an ordinary sum is below its last bit.)
+    template <int V>
+    __device__ __forceinline__ void add(const float (&u)[V])
+    {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            s = fmaf(u[k], u[k], s);
+        if (s > 0x1p-90f && s < 0x1p100f)
+            mid += s;
+        else
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                add(u[k]);
+    }
+    __device__ __forceinline__ double total() const
+    {
+        return static_cast<double>(big) * 0x1p140 + mid + static_cast<double>(small) * 0x1p-180;
+    }
+};
+
+// u * factor in fp32 for a factor that fp32 may not hold: a power of two near its root first, which is
+// exact, so that neither factor nor product leaves the range where the result does not.
+struct Scale {
+    float first, second;
+    __device__ __forceinline__ explicit Scale(double factor)
+    {
+        int e;
+        frexp(factor, &e);  // 0 for 0, infinities and NaN: they then pass through `second`
+        e = isfinite(factor) ? e / 2 : 0;
+        first = static_cast<float>(ldexp(1.0, e));
+        second = static_cast<float>(ldexp(factor, -e));
+    }
+    __device__ __forceinline__ Scale(float f, float s) : first(f), second(s) {}
+    __device__ __forceinline__ float operator()(float u) const { return u * first * second; }
+};
 
 // Updates the momentum and sums u^2 over part blockIdx.x of matrix blockIdx.y. V elements at a
 // time: 8 when every matrix starts on a 32-byte boundary, else 1.
@@ -121,7 +183,7 @@ __global__ void __launch_bounds__(256)
     const G *g = static_cast<const G *>(a.grad) + base;
     float *m = a.momentum ? a.momentum + base : nullptr;
     const int64_t step = static_cast<int64_t>(a.parts) * 256 * V;
-    double sum = 0.0;
+    Squares squares;
     for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * V; i < elems; i += step) {
         float u[V];
         load_gv<V>(g, i, u);
@@ -143,10 +205,9 @@ __global__ void __launch_bounds__(256)
                     m[i + k] = mv[k];
             }
         }
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-            sum += static_cast<double>(u[k]) * u[k];
+        squares.add(u);
     }
+    double sum = squares.total();
     for (int o = 16; o > 0; o >>= 1)
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if ((threadIdx.x & 31) == 0)
@@ -182,7 +243,7 @@ __global__ void __launch_bounds__(256)
         inv_s = static_cast<double>(kSx) / (sqrt(s) + a.eps);
     }
     __syncthreads();
-    const double inv = inv_s;
+    const Scale scale(inv_s);
     const int64_t base = static_cast<int64_t>(blockIdx.y) * a.rows * a.cols;
     const G *g = static_cast<const G *>(a.grad) + base;
     const float *m = a.momentum ? a.momentum + base : nullptr;
@@ -217,7 +278,7 @@ __global__ void __launch_bounds__(256)
         alignas(16) __half hi[8], lo[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            split_f16(static_cast<float>(u[k] * inv), hi[k], lo[k]);
+            split_f16(scale(u[k]), hi[k], lo[k]);
         const int64_t at = blockIdx.y * a.x_mat + row * a.x_pitch + col;
         *reinterpret_cast<uint4 *>(a.xh + at) = *reinterpret_cast<const uint4 *>(hi);
         *reinterpret_cast<uint4 *>(a.xl + at) = *reinterpret_cast<const uint4 *>(lo);
@@ -780,6 +841,520 @@ cudaError_t launch_gemm(const CUtensorMap &a_km, const CUtensorMap &a_mn, const 
                             b_km, b_mn, em, a, dc.wait);
 }
 
+// --------------------------------------------------------------------------- short matrices
+// p <= 128: a whole call in one launch, a cluster of C CTAs per matrix. CTA c holds columns [c W, (c + 1) W)
+// of X (rows of the input, for a tall matrix) for all steps: X in fp32 in tensor memory, one row per
+// lane, and its fp16 rounding in shared memory, a buffer that serves the Gram product K-major and the
+// update MN-major. Per step: A's partial products (M = N = 128, K = W), summed over the cluster through distributed
+// shared memory (each CTA a share of the elements, in rank order) and handed to every CTA as hi and lo; A A, B and
+// the update in each CTA for its own columns. What is exact and what is rounded is as in the products
+// below, but that X is fp32 itself. In place of 17 launches, whose latency bounds such matrices: 32 x
+// 128 x 256 99 -> 37 us, 1 x 128 x 1024 112 -> 56 us.
+constexpr int kShortThreads = 512;
+constexpr int kShortMaxP = 128;
+constexpr int kShortMaxW = 256;    // columns of a CTA: X and the update's accumulator share tensor memory
+constexpr int kShortMaxC = 8;      // CTAs of a cluster
+constexpr uint32_t kChunk = 16384; // 128 rows x 64 columns fp16
+constexpr uint32_t kShortXh = 0;                      // 4 chunks
+constexpr uint32_t kShortAh = 4 * kChunk;             // 2 chunks
+constexpr uint32_t kShortAl = kShortAh + 2 * kChunk;  // 2 chunks
+constexpr uint32_t kShortRed = kShortAl + 2 * kChunk; // this CTA's part of A, fp32; then B, fp16
+constexpr uint32_t kShortStage = kShortAh;            // the first X before it is scaled, then A, B's place
+constexpr uint32_t kShortVec = kShortStage + kShortMaxP * (kShortMaxW + 4) * 4;  // ra, rb [128] floats
+static_assert(kShortVec >= kShortRed + 4 * kChunk, "the stage covers the buffers behind Xh");
+constexpr uint32_t kShortMisc = kShortVec + 1024;
+constexpr uint32_t kShortSmem = kShortMisc + 512 + 1024;
+static_assert(kShortSmem <= static_cast<uint32_t>(kMaxDynSmem), "shared memory");
+static_assert(kShortAh + kShortMaxP * (kShortMaxW + 8) * 2 <= kShortVec, "the result is staged behind X");
+
+struct ShortArgs {
+    const void *grad;
+    float *momentum;
+    __nv_bfloat16 *out;
+    int rows, cols, p, W, steps, nesterov;
+    float a, b, c, out_scale, beta;
+    double eps;
+};
+
+__device__ __forceinline__ uint32_t cluster_nctarank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void fence_proxy_async_all()
+{
+    asm volatile("fence.proxy.async;" ::: "memory");
+}
+
+__device__ __forceinline__ float4 dsmem_ld_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ double dsmem_ld_f64(uint32_t addr)
+{
+    double v;
+    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void dsmem_st_u2(uint32_t addr, uint32_t x, uint32_t y)
+{
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
+
+__device__ __forceinline__ void dsmem_st_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// MN-major operand like sdesc_mn, its 64-element MN chunks a whole chunk (128 K rows) apart.
+__device__ __forceinline__ uint64_t sdesc_mn_chunk(uint32_t saddr)
+{
+    uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFF);
+    d |= static_cast<uint64_t>(kChunk >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= 1ull << 46;
+    d |= 2ull << 61;
+    return d;
+}
+
+// Byte offset of columns [col, col + 8) of row r in a buffer of 64-column chunks (128-byte swizzle).
+__device__ __forceinline__ uint32_t chunk_at8(int r, int col)
+{
+    return static_cast<uint32_t>(col >> 6) * kChunk + r * 128 + ((((col >> 3) & 7) ^ (r & 7)) << 4);
+}
+
+template <typename G, bool TALL, int V>
+__global__ void __launch_bounds__(kShortThreads, 1)
+    orth_short_kernel(const ShortArgs a, const WaitCfg wc)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float *ra = reinterpret_cast<float *>(smem + kShortVec), *rb = ra + 128;
+    uint64_t *mma = reinterpret_cast<uint64_t *>(smem + kShortMisc);
+    uint32_t *holder = reinterpret_cast<uint32_t *>(smem + kShortMisc + 8);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kShortMisc + 12);
+    double *part = reinterpret_cast<double *>(smem + kShortMisc + 16);   // [1] this CTA's sum of squares
+    float *factors = reinterpret_cast<float *>(smem + kShortMisc + 24);  // [2] of the first X's scale
+    double *warp_sum = reinterpret_cast<double *>(smem + kShortMisc + 64);  // [16]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int C = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
+    const int mat = blockIdx.x / C;
+    const int p = a.p, W = a.W, q = TALL ? a.rows : a.cols;
+    const int q0 = rank * W, w = q - q0 < W ? (q - q0 > 0 ? q - q0 : 0) : W;  // this CTA's columns of X
+    if (threadIdx.x == 0) {
+        mbar_init(mma, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(holder, 512);
+        tmem_relinquish();
+    }
+    if (threadIdx.x < 256)
+        ra[threadIdx.x] = 0.0f;  // ra and rb: rows that A and B do not have stay zero
+
+    // u (and the momentum) in the order of memory, summed and staged as floats [p][pitch]; V elements
+    // an access, kLoads accesses in flight
+    float *stage = reinterpret_cast<float *>(smem + kShortStage);
+    const int pitch = TALL ? W + 1 : W + 4;  // few bank conflicts of the transposing stores; of vector ones none
+    const int64_t base = static_cast<int64_t>(mat) * a.rows * a.cols;
+    const int mr = TALL ? w : p, mc = TALL ? p : w;  // memory rows and columns of this CTA's part
+    const int64_t off = base + (TALL ? static_cast<int64_t>(q0) * a.cols : q0);
+    {
+        constexpr int kLoads = 4;
+        const G *g = static_cast<const G *>(a.grad) + off;
+        float *m = a.momentum ? a.momentum + off : nullptr;
+        const int per_row = mc / V > 0 ? mc / V : 1, items = mc > 0 ? mr * per_row : 0;
+        // a thread's items are kShortThreads apart: their rows and columns by addition
+        const int dr = kShortThreads / per_row, dc = kShortThreads - dr * per_row;
+        int row = threadIdx.x / per_row, col = threadIdx.x - row * per_row;
+        Squares squares;
+        for (int i0 = threadIdx.x; i0 < items; i0 += kLoads * kShortThreads) {
+            float u[kLoads][V], mv[kLoads][V];
+            int at[kLoads], place[kLoads];  // offsets in memory (below 2^31: at most 128 rows or columns) and in the stage
+#pragma unroll
+            for (int l = 0; l < kLoads; ++l) {
+                at[l] = row * a.cols + col * V;
+                place[l] = TALL ? col * V * pitch + row : row * pitch + col * V;
+                if (i0 + l * kShortThreads < items) {
+                    load_gv<V>(g, at[l], u[l]);
+                    if (m)
+                        load_gv<V>(m, at[l], mv[l]);
+                }
+                row += dr;
+                col += dc;
+                if (col >= per_row) {
+                    col -= per_row;
+                    ++row;
+                }
+            }
+#pragma unroll
+            for (int l = 0; l < kLoads; ++l) {
+                if (i0 + l * kShortThreads >= items)
+                    break;
+                if (m) {
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        mv[l][k] = fmaf(a.beta, mv[l][k], u[l][k]);
+                        u[l][k] = a.nesterov ? fmaf(a.beta, mv[l][k], u[l][k]) : mv[l][k];
+                    }
+                    if (V == 4)
+                        *reinterpret_cast<float4 *>(m + at[l]) =
+                            make_float4(mv[l][0], mv[l][1 % V], mv[l][2 % V], mv[l][3 % V]);
+                    else
+                        m[at[l]] = mv[l][0];
+                }
+                squares.add(u[l]);
+                if (TALL) {
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        stage[place[l] + k * pitch] = u[l][k];
+                } else if (V == 4) {
+                    *reinterpret_cast<float4 *>(stage + place[l]) =
+                        make_float4(u[l][0], u[l][1 % V], u[l][2 % V], u[l][3 % V]);
+                } else {
+                    stage[place[l]] = u[l][0];
+                }
+            }
+        }
+        double sum = squares.total();
+        for (int o = 16; o > 0; o >>= 1)
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (lane == 0)
+            warp_sum[warp] = sum;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x == 0) {
+        double s = 0.0;
+        for (int i = 0; i < kShortThreads / 32; ++i)
+            s += warp_sum[i];
+        *part = s;
+    }
+    cluster_sync_all();
+    const uint32_t tmem = *holder;
+    if (threadIdx.x == 0) {
+        double total = 0.0;
+        for (int c = 0; c < C; ++c)
+            total += dsmem_ld_f64(dsmem_addr(smem_u32(part), c));
+        // X lives in tensor memory columns [0, W) as X kSb kSx, the scale of the update's accumulator
+        const Scale s(static_cast<double>(kSb) * kSx / (sqrt(total) + a.eps));
+        factors[0] = s.first;
+        factors[1] = s.second;
+    }
+    __syncthreads();
+    const Scale scale(factors[0], factors[1]);
+    const int r = (warp & 3) * 32 + lane;      // this thread's row of X, A and B
+    const int cg = warp >> 2;                  // its quarter of a row's columns
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int wq = W / 4;                      // a multiple of 16
+    // (loops over a row's columns are not unrolled: each runs once or twice, and instructions that
+    // are fetched to run once cost more than the loop)
+#pragma unroll 1
+    for (int i = 0; i < wq; i += 16) {
+        const int col = cg * wq + i;
+        const float *from = stage + r * pitch + col;
+        uint32_t bits[16], h[8];
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (r < p) {
+                if (TALL)  // a row of the stage is W + 1 floats: no alignment
+                    v = make_float4(from[k], from[k + 1], from[k + 2], from[k + 3]);
+                else
+                    v = *reinterpret_cast<const float4 *>(from + k);
+            }
+            // what lies behind column w was never staged
+            const float x[4] = {col + k < w ? scale(v.x) : 0.0f, col + k + 1 < w ? scale(v.y) : 0.0f,
+                                col + k + 2 < w ? scale(v.z) : 0.0f, col + k + 3 < w ? scale(v.w) : 0.0f};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                bits[k + e] = __float_as_uint(x[e]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const __half2 t = __floats2half2_rn(x[2 * e] * (1.0f / kSb), x[2 * e + 1] * (1.0f / kSb));
+                h[k / 2 + e] = *reinterpret_cast<const uint32_t *>(&t);
+            }
+        }
+        tmem_store16(tmem + lanes + col, bits);
+        *reinterpret_cast<uint4 *>(smem + kShortXh + chunk_at8(r, col)) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(smem + kShortXh + chunk_at8(r, col + 8)) = make_uint4(h[4], h[5], h[6], h[7]);
+    }
+    __syncthreads();  // the stage gives way to the buffers
+    tmem_store_wait();
+
+    const int np = (p + 15) & ~15;  // A and B: rows and columns in use
+    const uint32_t t_acc = tmem + kShortMaxW, t_a = t_acc, t_a2 = t_acc + 128;
+    uint32_t phase = 0, issued = 1;  // parity of the latest product that thread 0 issued
+    // Every thread's writes made visible to the tensor core, one thread's MMAs, every thread behind them.
+    // After an expired wait the rest runs through without waiting (the results are void).
+    const auto product = [&](auto issue) {
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (threadIdx.x == 0 && !*abort_flag) {
+            tc_fence_after();
+            issue();
+            umma_commit(mma);
+            issued = phase;
+        }
+        warp_wait(mma, phase, wc, abort_flag);
+        phase ^= 1;
+        tc_fence_after();
+    };
+    const uint32_t xh = smem_u32(smem + kShortXh), ah = smem_u32(smem + kShortAh), bh = smem_u32(smem + kShortRed);
+
+    for (int step = 0; step < a.steps; ++step) {
+        product([&]() {
+            for (int ks = 0; ks < W / 16; ++ks) {
+                const uint64_t d = sdesc_kmajor_sw128(xh + (ks >> 2) * kChunk) + 2 * (ks & 3);
+                umma_bf16(t_a, d, d, idesc_f16_f32(128, np), ks != 0);
+            }
+        });
+        if (C > 1) {
+            // this CTA's part of A, then its share of the sum, to every CTA
+            float *red = reinterpret_cast<float *>(smem + kShortRed);
+            if (cg * 32 < np) {
+                float v[32];
+                tmem_load32(t_a + lanes + cg * 32, v);
+                // 16-byte columns rotated by the row, which keeps a column's stores off one bank
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<float4 *>(red + r * 128 + ((cg * 8 + k + r) & 31) * 4) =
+                        make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
+            cluster_sync_all();
+            const int per_row = np / 4;
+            for (int e = rank * kShortThreads + threadIdx.x; e < p * per_row; e += C * kShortThreads) {
+                const int i = e / per_row, j = (e - i * per_row) * 4;
+                const uint32_t at = smem_u32(red + i * 128 + ((j / 4 + i) & 31) * 4);
+                float4 v[kShortMaxC];
+#pragma unroll
+                for (int c = 0; c < kShortMaxC; ++c)
+                    if (c < C)
+                        v[c] = dsmem_ld_f4(dsmem_addr(at, c));
+                float4 s4 = v[0];
+#pragma unroll
+                for (int c = 1; c < kShortMaxC; ++c)
+                    if (c < C) {
+                        s4.x += v[c].x;
+                        s4.y += v[c].y;
+                        s4.z += v[c].z;
+                        s4.w += v[c].w;
+                    }
+                const float f = kSa / (kSx * kSx);
+                uint32_t h0, l0, h1, l1;
+                const float2 r0 = split_pair(s4.x * f, s4.y * f, h0, l0), r1 = split_pair(s4.z * f, s4.w * f, h1, l1);
+                const uint32_t o = chunk_at8(i, j) + (j & 7) * 2;
+                const uint32_t la = smem_u32(smem + kShortAh + o), ll = smem_u32(smem + kShortAl + o);
+                const bool diag = i >= j && i < j + 4;
+                const float rest = i - j == 0 ? r0.x : (i - j == 1 ? r0.y : (i - j == 2 ? r1.x : r1.y));
+#pragma unroll 1
+                for (int c = 0; c < C; ++c) {
+                    dsmem_st_u2(dsmem_addr(la, c), h0, h1);
+                    dsmem_st_u2(dsmem_addr(ll, c), l0, l1);
+                    if (diag)
+                        dsmem_st_f32(dsmem_addr(smem_u32(ra + i), c), rest);
+                }
+            }
+            if (step == 0)  // rows from p on of the operand stay zero
+                for (int e = threadIdx.x; e < (128 - p) * 16; e += kShortThreads) {
+                    const int i = p + e / 16;
+                    *reinterpret_cast<uint4 *>(smem + kShortAh + chunk_at8(i, e % 16 * 8)) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(smem + kShortAl + chunk_at8(i, e % 16 * 8)) = make_uint4(0, 0, 0, 0);
+                }
+            fence_proxy_async_all();
+            cluster_sync_all();
+        } else {
+            if (cg * 32 < np) {
+                float v[32];
+                tmem_load32(t_a + lanes + cg * 32, v);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t h[4], l[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float f = kSa / (kSx * kSx);
+                        const int col = cg * 32 + 8 * k + 2 * i;
+                        const float2 rest = split_pair(v[8 * k + 2 * i] * f, v[8 * k + 2 * i + 1] * f, h[i], l[i]);
+                        if (col == r && r < p)
+                            ra[r] = rest.x;
+                        if (col + 1 == r && r < p)
+                            ra[r] = rest.y;
+                    }
+                    const uint32_t o = chunk_at8(r, cg * 32 + 8 * k);
+                    *reinterpret_cast<uint4 *>(smem + kShortAh + o) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4 *>(smem + kShortAl + o) = make_uint4(l[0], l[1], l[2], l[3]);
+                }
+            }
+        }
+        product([&]() {
+            for (int ks = 0; ks < np / 16; ++ks) {
+                const uint64_t d = sdesc_kmajor_sw128(ah + (ks >> 2) * kChunk) + 2 * (ks & 3);
+                umma_bf16(t_a2, d, d, idesc_f16_f32(128, np), ks != 0);
+            }
+        });
+        const float ra_row = ra[r];
+        if (cg * 32 < np) {
+            float v[32];
+            tmem_load32(t_a2 + lanes + cg * 32, v);
+            const float f = a.c * (kSb / kSa) * (1.0f / kSa);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t o = chunk_at8(r, cg * 32 + 8 * k);
+                const uint4 h4 = *reinterpret_cast<const uint4 *>(smem + kShortAh + o);
+                const uint4 l4 = *reinterpret_cast<const uint4 *>(smem + kShortAl + o);
+                uint32_t h[4] = {h4.x, h4.y, h4.z, h4.w}, l[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int col = cg * 32 + 8 * k + 2 * i;
+                    const float2 old = join_f16(h[i], l[i]);
+                    const float2 rc = *reinterpret_cast<const float2 *>(ra + col);
+                    const float2 rest =
+                        split_pair(fmaf(a.b, old.x, f * fmaf(ra_row + rc.x, old.x, v[8 * k + 2 * i])),
+                                   fmaf(a.b, old.y, f * fmaf(ra_row + rc.y, old.y, v[8 * k + 2 * i + 1])), h[i], l[i]);
+                    if (col == r && r < p)
+                        rb[r] = rest.x;
+                    if (col + 1 == r && r < p)
+                        rb[r] = rest.y;
+                }
+                *reinterpret_cast<uint4 *>(smem + kShortRed + o) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+        }
+        product([&]() {
+            for (int ks = 0; ks < np / 16; ++ks)
+                umma_bf16(t_acc, sdesc_kmajor_sw128(bh + (ks >> 2) * kChunk) + 2 * (ks & 3),
+                          sdesc_mn_chunk(xh + ks * 2048), idesc_f16_f32(128, W) | 1u << 16, ks != 0);
+        });
+        const float f = fmaf(rb[r], 1.0f / kSb, a.a);
+        const bool last = step + 1 == a.steps;
+        __nv_bfloat16 *result = reinterpret_cast<__nv_bfloat16 *>(smem + kShortAh);
+#pragma unroll 1
+        for (int i = 0; i < wq; i += 16) {
+            const int col = cg * wq + i;
+            float old[16], acc[16];
+            tmem_load16(tmem + lanes + col, old);
+            tmem_load16(t_acc + lanes + col, acc);
+            uint32_t bits[16], h[8];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                old[k] = fmaf(f, old[k], acc[k]);
+                bits[k] = __float_as_uint(old[k]);
+            }
+            if (last) {  // staged where A was: tall as memory has it, [w][p], wide in rows of W + 8
+                if (TALL) {
+                    if (r < p)
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (col + k < w)
+                                result[(col + k) * p + r] = __float2bfloat16_rn(old[k] * a.out_scale);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const __nv_bfloat162 v =
+                            __floats2bfloat162_rn(old[2 * k] * a.out_scale, old[2 * k + 1] * a.out_scale);
+                        h[k] = *reinterpret_cast<const uint32_t *>(&v);
+                    }
+                    uint4 *to = reinterpret_cast<uint4 *>(result + r * (W + 8) + col);
+                    to[0] = make_uint4(h[0], h[1], h[2], h[3]);
+                    to[1] = make_uint4(h[4], h[5], h[6], h[7]);
+                }
+                continue;
+            }
+            tmem_store16(tmem + lanes + col, bits);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const __half2 v = __floats2half2_rn(old[2 * k] * (1.0f / kSb), old[2 * k + 1] * (1.0f / kSb));
+                h[k] = *reinterpret_cast<const uint32_t *>(&v);
+            }
+            *reinterpret_cast<uint4 *>(smem + kShortXh + chunk_at8(r, col)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(smem + kShortXh + chunk_at8(r, col + 8)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        if (!last)
+            tmem_store_wait();
+    }
+    __syncthreads();
+    {
+        const __nv_bfloat16 *result = reinterpret_cast<const __nv_bfloat16 *>(smem + kShortAh);
+        __nv_bfloat16 *o = a.out + off;
+        const int count = mr * mc;
+        const bool wide = reinterpret_cast<uintptr_t>(o) % 16 == 0 && (TALL || (a.cols % 8 == 0 && mc % 8 == 0));
+        if (wide) {
+            const int per_row = TALL ? 1 : mc / 8;
+            const int items = TALL ? count / 8 : mr * per_row;
+            for (int i = threadIdx.x; i < items; i += kShortThreads) {
+                const int row = TALL ? 0 : i / per_row;
+                const int col = TALL ? i * 8 : (i - row * per_row) * 8;
+                *reinterpret_cast<uint4 *>(o + static_cast<int64_t>(row) * a.cols + col) =
+                    *reinterpret_cast<const uint4 *>(result + row * (W + 8) + col);
+            }
+            if (TALL)
+                for (int i = count / 8 * 8 + threadIdx.x; i < count; i += kShortThreads)
+                    o[i] = result[i];
+        } else {
+            for (int i = threadIdx.x; i < count; i += kShortThreads) {
+                const int row = i / mc, col = i - row * mc;
+                o[static_cast<int64_t>(row) * a.cols + col] = result[TALL ? i : row * (W + 8) + col];
+            }
+        }
+    }
+    if (threadIdx.x == 0 && *abort_flag)
+        mbar_wait_drain(mma, issued, wc);  // a product that was given up on may still be running
+    tc_fence_before();
+    cluster_sync_all();  // no CTA leaves while a peer may still reach its shared memory
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// -------------------------------------------------------------------------------- host, short
+// Columns per CTA and CTAs per matrix; false if the matrix takes the products' path.
+bool short_split(int p, int q, int &W, int &C)
+{
+    if (p > kShortMaxP || q > kShortMaxC * kShortMaxW)
+        return false;
+    C = (q + kShortMaxW - 1) / kShortMaxW;
+    W = ((q + C - 1) / C + 63) / 64 * 64;
+    return true;
+}
+
+template <typename G, bool TALL>
+cudaError_t launch_short(const ShortArgs &a, int n, int C, const WaitCfg &wc, cudaStream_t stream)
+{
+    // four elements an access where every memory row keeps that alignment
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.grad) * (16 / (4 * sizeof(G))) |
+                           reinterpret_cast<uintptr_t>(a.momentum);
+    auto kernel = a.cols % 4 == 0 && bits % 16 == 0 ? orth_short_kernel<G, TALL, 4> : orth_short_kernel<G, TALL, 1>;
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kShortSmem));
+    if (err != cudaSuccess)
+        return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(n) * C);
+    cfg.blockDim = dim3(kShortThreads);
+    cfg.dynamicSmemBytes = kShortSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, wc);
+}
+
 // ------------------------------------------------------------------------------------ host
 constexpr int kMaxSide = 16384;
 constexpr int kMaxSteps = 32;
@@ -1000,6 +1575,18 @@ moe_status_t moe_orthogonalize(const moe_orthogonalize_desc *desc, const void *g
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint8_t *w = static_cast<uint8_t *>(ws);
     const int64_t elems = static_cast<int64_t>(d.rows) * d.cols;
+    int W, C;
+    if (short_split(L.p, d.rows < d.cols ? d.cols : d.rows, W, C)) {
+        const ShortArgs sa{grad, momentum, reinterpret_cast<__nv_bfloat16 *>(out), d.rows, d.cols, L.p, W, d.steps,
+                           d.nesterov, d.a, d.b, d.c, d.scale / (kSx * kSb), d.beta, d.eps};
+        const bool f32 = d.dtype == MOE_DTYPE_F32;
+        const cudaError_t e =
+            d.rows > d.cols ? (f32 ? launch_short<float, true>(sa, d.n, C, dc.wait, s)
+                                   : launch_short<__nv_bfloat16, true>(sa, d.n, C, dc.wait, s))
+                            : (f32 ? launch_short<float, false>(sa, d.n, C, dc.wait, s)
+                                   : launch_short<__nv_bfloat16, false>(sa, d.n, C, dc.wait, s));
+        return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
     for (int first = 0; first < d.n; first += L.chunk) {
         const int n = d.n - first < L.chunk ? d.n - first : L.chunk;
         PrepArgs pa{};

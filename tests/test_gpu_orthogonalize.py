@@ -59,7 +59,10 @@ def gauss(n, rows, cols, seed=0):
 
 SIZES = [(3, 128, 256), (2, 256, 128), (1, 1, 1), (2, 1, 77), (2, 77, 1), (3, 33, 40), (2, 40, 33), (2, 130, 129),
          (1, 129, 131), (4, 64, 64), (1, 200, 1000), (1, 1000, 200), (2, 384, 257), (1, 513, 640), (1, 640, 513),
-         (1, 1281, 700), (1, 700, 1281), (150, 16, 24)]
+         (1, 1281, 700), (1, 700, 1281), (150, 16, 24),
+         # short sides up to 128: a cluster per matrix, up to 2048 on the long side; beyond, the products
+         (3, 100, 256), (2, 100, 257), (2, 600, 100), (1, 128, 2048), (1, 2047, 127), (2, 17, 1100), (1, 128, 2049),
+         (1, 2100, 64)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -79,7 +82,7 @@ def test_layer_sizes(rows, cols):
 
 
 @pytest.mark.parametrize("rank", [1, 5, 40])
-@pytest.mark.parametrize("rows,cols", [(160, 416), (416, 160), (1280, 1408)])
+@pytest.mark.parametrize("rows,cols", [(160, 416), (416, 160), (1280, 1408), (60, 200), (700, 128)])
 def test_gradients_of_few_tokens(rows, cols, rank):
     """A gradient of few tokens has a low rank: nothing may grow outside its range."""
     g = gauss(2, rows, rank, 1) @ gauss(2, rank, cols, 2)
@@ -88,7 +91,7 @@ def test_gradients_of_few_tokens(rows, cols, rank):
 
 @pytest.mark.parametrize("nesterov", [True, False])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("rows,cols", [(96, 200), (131, 77)])
+@pytest.mark.parametrize("rows,cols", [(96, 200), (131, 77), (131, 177), (600, 96)])
 def test_momentum(rows, cols, dtype, nesterov):
     o = moe.Orthogonalizer(3, rows, cols, grad_dtype=dtype, beta=0.9, nesterov=nesterov)
     m = gauss(3, rows, cols, 4)
