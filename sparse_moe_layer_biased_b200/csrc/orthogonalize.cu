@@ -319,6 +319,7 @@ struct OrthGeo {
     static constexpr uint32_t kSmem = kMiscOff + 16 + 1024;
     static constexpr uint32_t kTmemCols = 2 * kTile;
     static_assert(kSmem <= static_cast<uint32_t>(kMaxDynSmem), "ring exceeds shared memory");
+    static_assert(kBlocks >= kGroups && (kGroups & (kGroups - 1)) == 0, "a group's blocks are kGroups apart");
 };
 
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N)
@@ -778,7 +779,9 @@ __global__ void __launch_bounds__(OrthGeo<PAIR>::kThreads, 1)
             const int nb = row0 < M ? ((N - n0 < TILE ? N - n0 : TILE) + 31) / 32 : 0;
             ok = warp_wait(&accf[buf], (tc >> 1) & 1, wc, abort_flag);
             tc_fence_after();
-            for (int b = grp; b < nb && ok; b += G::kGroups) {
+            // Groups go by the CTA's block number, so that a group's next block is never more than
+            // kBlocks behind its last one: a barrier's parity could not tell phases two apart.
+            for (int b = (grp - i0) & (G::kGroups - 1); b < nb && ok; b += G::kGroups) {
                 const int i = i0 + b, u = i % G::kBlocks;
                 ok = warp_wait(&bfull[u], (i / G::kBlocks) & 1, wc, abort_flag);
                 if (!ok)

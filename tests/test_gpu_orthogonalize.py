@@ -198,3 +198,11 @@ def test_misaligned_inputs():
 def test_no_matrices():
     o = moe.Orthogonalizer(0, 16, 32)
     assert o.orthogonalize(torch.empty((0, 16, 32), device="cuda")).shape == (0, 16, 32)
+
+
+@pytest.mark.parametrize("rows,cols", [(300, 337), (600, 340), (340, 600), (200, 2000)])
+def test_many_tiles_a_cta_with_short_ones_among_them(rows, cols):
+    """More matrices than CTAs, tiles of one to four (or eight) column blocks in turn."""
+    n = 170
+    g = gauss(n, rows, cols, 17)
+    check(moe.Orthogonalizer(n, rows, cols).orthogonalize(g), reference(g))
