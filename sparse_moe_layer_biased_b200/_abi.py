@@ -134,6 +134,10 @@ def _p(t):
     return t.data_ptr()
 
 
+def _nbytes(ws):
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
 def _stream(stream):
     if stream is None:
         # the handle of torch.cuda.current_stream() without the Stream object around it, which
@@ -289,21 +293,24 @@ def moe_sort_workspace_size(desc: TokenDesc) -> int:
 def moe_sort_tokens(desc, x, topk_idx, x_sorted, offsets, slot_of, ws, stream=None):
     """Rows of x sorted by expert, with the places and offsets (entries with ids outside [0, E) dropped)."""
     _check("moe_sort_tokens", lib().moe_sort_tokens(
-        ctypes.byref(desc), _p(x), _p(topk_idx), _p(x_sorted), _p(offsets), _p(slot_of), _p(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+        ctypes.byref(desc), _p(x), _p(topk_idx), _p(x_sorted), _p(offsets), _p(slot_of), _p(ws), _nbytes(ws),
+        _stream(stream)))
 
 
 def moe_sort_tokens_backward(desc, dx_sorted, slot_of, dx, stream=None):
+    """dx[t] = the sum of the rows of token t's entries."""
     _check("moe_sort_tokens_backward", lib().moe_sort_tokens_backward(
         ctypes.byref(desc), _p(dx_sorted), _p(slot_of), _p(dx), _stream(stream)))
 
 
 def moe_unsort_tokens(desc, y_sorted, slot_of, topk_w, add, y, stream=None):
+    """Rows back to their tokens, weighted (topk_w None: 1) and added to `add` (None: 0)."""
     _check("moe_unsort_tokens", lib().moe_unsort_tokens(
         ctypes.byref(desc), _p(y_sorted), _p(slot_of), _p(topk_w), _p(add), _p(y), _stream(stream)))
 
 
 def moe_unsort_tokens_backward(desc, dy, y_sorted, slot_of, topk_w, dy_sorted, dtopk_w, stream=None):
+    """Gradients of the weighted unsort (either output may be None)."""
     _check("moe_unsort_tokens_backward", lib().moe_unsort_tokens_backward(
         ctypes.byref(desc), _p(dy), _p(y_sorted), _p(slot_of), _p(topk_w), _p(dy_sorted), _p(dtopk_w),
         _stream(stream)))
@@ -319,5 +326,4 @@ def moe_orthogonalize_workspace_size(desc: OrthogonalizeDesc) -> int:
 def moe_orthogonalize(desc, grad, momentum, out, ws, stream=None):
     """Orthogonalised updates of a stack of matrices (momentum updated in place, or None)."""
     _check("moe_orthogonalize", lib().moe_orthogonalize(
-        ctypes.byref(desc), _p(grad), _p(momentum), _p(out), _p(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+        ctypes.byref(desc), _p(grad), _p(momentum), _p(out), _p(ws), _nbytes(ws), _stream(stream)))

@@ -16,6 +16,8 @@
 // Every kernel reads and writes each row once and does a handful of operations per element: HBM
 // bandwidth bounds the large calls, launch and dependent-load latency the small ones. Sums
 // run in fp32, over j in rank order, and round once to the rows' type.
+#include <atomic>
+
 #include <cuda_fp16.h>
 
 #include "../../include/moe_b200.h"
@@ -909,6 +911,22 @@ bool aligned_to(const void *p, int bytes)
     return reinterpret_cast<uintptr_t>(p) % bytes == 0;
 }
 
+// SMs of the current device: an attribute that does not change, asked for once per device.
+moe_status_t sm_count(int &sms)
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return MOE_ERR_CUDA;
+    sms = known[dev].load(std::memory_order_relaxed);
+    if (sms == 0) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        known[dev].store(sms, std::memory_order_relaxed);
+    }
+    return MOE_OK;
+}
+
 moe_status_t launched(cudaError_t e)
 {
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -958,13 +976,13 @@ moe_status_t moe_sort_tokens(const moe_token_desc *desc, const void *x, const in
         return st;
     if (ws_bytes < need)
         return MOE_ERR_WORKSPACE;
-    DeviceContext dc;
-    if ((st = static_cast<moe_status_t>(device_context(dc))) != MOE_OK)
+    int sms = 0;
+    if ((st = sm_count(sms)) != MOE_OK)
         return st;
     const int64_t row = static_cast<int64_t>(desc->H) * elem;
     auto go = [&](auto u) {
         return launch_sort<decltype(u)>(x, topk_idx, desc->T, desc->k, desc->E, row, x_sorted, offsets, slot_of, ws,
-                                        dc.num_sms, s);
+                                        sms, s);
     };
     switch (pack_bytes(row, elem, {x, x_sorted})) {
     case 16: return launched(go(uint4{}));
@@ -988,14 +1006,14 @@ moe_status_t moe_unsort_tokens(const moe_token_desc *desc, const void *y_sorted,
     if (!aligned_to(y_sorted, elem) || !aligned_to(y, elem) || !aligned_to(add, elem) || !aligned_to(slot_of, 4) ||
         !aligned_to(topk_w, 4))
         return MOE_ERR_UNSUPPORTED;
-    DeviceContext dc;
-    if ((st = static_cast<moe_status_t>(device_context(dc))) != MOE_OK)
+    int sms = 0;
+    if ((st = sm_count(sms)) != MOE_OK)
         return st;
     const int bytes = pack_bytes(static_cast<int64_t>(desc->H) * elem, elem, {y_sorted, add, y});
     return launched(by_type(desc->dtype, bytes, [&](auto tag) {
         using V = decltype(tag);
         return unsort_vec<typename V::type, V::vec>(y_sorted, slot_of, topk_w, add, desc->T, desc->k, desc->H, y,
-                                                    dc.num_sms, static_cast<cudaStream_t>(stream));
+                                                    sms, static_cast<cudaStream_t>(stream));
     }));
 }
 
@@ -1021,14 +1039,14 @@ moe_status_t moe_unsort_tokens_backward(const moe_token_desc *desc, const void *
     if (!aligned_to(dy, elem) || !aligned_to(y_sorted, elem) || !aligned_to(dy_sorted, elem) ||
         !aligned_to(slot_of, 4) || !aligned_to(topk_w, 4) || !aligned_to(dtopk_w, 4))
         return MOE_ERR_UNSUPPORTED;
-    DeviceContext dc;
-    if ((st = static_cast<moe_status_t>(device_context(dc))) != MOE_OK)
+    int sms = 0;
+    if ((st = sm_count(sms)) != MOE_OK)
         return st;
     const int bytes = pack_bytes(static_cast<int64_t>(desc->H) * elem, elem, {dy, y_sorted, dy_sorted});
     return launched(by_type(desc->dtype, bytes, [&](auto tag) {
         using V = decltype(tag);
         return unsort_backward_vec<typename V::type, V::vec>(dy, y_sorted, slot_of, topk_w, desc->T, desc->k, desc->H,
-                                                             dy_sorted, dtopk_w, dc.num_sms,
+                                                             dy_sorted, dtopk_w, sms,
                                                              static_cast<cudaStream_t>(stream));
     }));
 }

@@ -11,13 +11,15 @@ PyTorch only allocates device memory and supplies the stream; the arithmetic run
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _abi
-from .tokens import check_tensor
+from .tokens import Caller, check_tensor
 
 
-class Orthogonalizer:
+class Orthogonalizer(Caller):
     """n matrices [rows, cols]: u = grad, or with momentum m <- beta m + grad and u = grad + beta m
     (nesterov) or m; X = u / (|u|_F + eps); `steps` times X <- a X + (b A + c A A) X with A = X X^T
     (of the shorter side), coeffs = (a, b, c); the update is bf16(scale X).
@@ -35,10 +37,7 @@ class Orthogonalizer:
         self.desc = _abi.OrthogonalizeDesc(n, rows, cols, _abi.DTYPES[grad_dtype], steps, *coeffs, eps, scale, beta,
                                            int(bool(nesterov)))
         nbytes = _abi.moe_orthogonalize_workspace_size(self.desc)
-        device = torch.device(device)
-        if device.type == "cuda" and device.index is None:
-            device = torch.device("cuda", torch.cuda.current_device())
-        self.device = device
+        super().__init__(device)
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
 
     def orthogonalize(self, grad: torch.Tensor, momentum: torch.Tensor | None = None, out: torch.Tensor | None = None,
@@ -46,15 +45,12 @@ class Orthogonalizer:
         """grad [n, rows, cols] of grad_dtype, momentum [n, rows, cols] fp32 (updated in place) or
         None -> the update [n, rows, cols] bf16, in `out` if given. Runs on the current stream of the
         tensors' device, or on `stream`."""
-        check_tensor(grad, "grad", self.shape, self.grad_dtype, self.device)
+        check_tensor(grad, "grad", self.shape, self.grad_dtype, self._dev)
         if momentum is not None:
-            check_tensor(momentum, "momentum", self.shape, torch.float32, self.device)
+            check_tensor(momentum, "momentum", self.shape, torch.float32, self._dev)
         if out is None:
             out = torch.empty(self.shape, dtype=torch.bfloat16, device=self.device)
-        check_tensor(out, "out", self.shape, torch.bfloat16, self.device)
-        if torch.cuda.current_device() == self.device.index:
-            _abi.moe_orthogonalize(self.desc, grad, momentum, out, self.ws, stream=stream)
-        else:
-            with torch.cuda.device(self.device):
-                _abi.moe_orthogonalize(self.desc, grad, momentum, out, self.ws, stream=stream)
+        check_tensor(out, "out", self.shape, torch.bfloat16, self._dev)
+        self._run(_abi.lib().moe_orthogonalize, stream, ctypes.byref(self.desc), grad.data_ptr(),
+                  None if momentum is None else momentum.data_ptr(), out.data_ptr(), self.ws.data_ptr(), self.ws.numel())
         return out

@@ -16,20 +16,49 @@ PyTorch only allocates device memory and supplies the stream; the arithmetic run
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _abi
 
 
-def check_tensor(t, name: str, shape, dtype, device) -> None:
-    """ValueError unless t is a contiguous tensor of this shape, type and device."""
-    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {device} is wanted, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}"
-                         f"{'' if t.is_contiguous() else ' (not contiguous)'}")
+def check_tensor(t, name: str, shape, dtype, index) -> None:
+    """ValueError unless t is a contiguous tensor of this shape and type on CUDA device `index` (-1: the host)."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{'the host' if index < 0 else f'cuda:{index}'} is wanted, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}{'' if t.is_contiguous() else ' (not contiguous)'}")
 
 
-class TokenSorter:
+def device_index(device) -> int:
+    """Index of a CUDA device (the current one if `device` names none), -1 for the host."""
+    device = torch.device(device)
+    if device.type != "cuda":
+        return -1
+    return torch.cuda.current_device() if device.index is None else device.index
+
+
+class Caller:
+    """Calls of the library for tensors of one device, with little host time: a small call's kernel is
+    over in 3 us, and a call through _abi's functions costs 2 us more than this."""
+
+    def __init__(self, device):
+        self._dev = device_index(device)
+        self.device = torch.device("cpu") if self._dev < 0 else torch.device("cuda", self._dev)
+        self._several = torch.cuda.device_count() > 1
+
+    def _run(self, fn, stream, *args) -> None:
+        """fn(*args, stream handle) with the device current, on `stream` or the device's current stream."""
+        if self._several and torch.cuda.current_device() != self._dev:
+            with torch.cuda.device(self._dev):
+                return self._run(fn, stream, *args)
+        status = fn(*args, _abi._raw_stream(self._dev) if stream is None else _abi._stream(stream))
+        if status:
+            raise _abi.MoeError(fn.__name__, status)
+
+
+class TokenSorter(Caller):
     """Sorts rows [T, H] of `dtype` (bf16, fp16 or fp32) of up to max_tokens tokens with k
     entries each over E experts. An entry whose id is outside [0, E) is dropped: it has no row, adds
     nothing and gets no gradient (a padded token; with expert parallelism an expert held
@@ -45,94 +74,85 @@ class TokenSorter:
         if dtype not in _abi.DTYPES:
             raise ValueError(f"rows of {dtype} are not supported")
         self.max_tokens, self.H, self.E, self.k, self.dtype = max_tokens, H, E, k, dtype
-        self._code = _abi.DTYPES[dtype]
-        self._last = None  # the latest call's descriptor
+        super().__init__(device)
         nbytes = _abi.moe_sort_workspace_size(self._desc(max_tokens))
-        device = torch.device(device)
-        if device.type == "cuda" and device.index is None:
-            device = torch.device("cuda", torch.cuda.current_device())
-        self.device = device
-        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        self._last = (-1, None)  # the latest call's token count, and its descriptor by reference
+        self._lib = _abi.lib()
 
     def _desc(self, T: int) -> _abi.TokenDesc:
-        d = self._last
-        if d is None or d.T != T:
-            d = self._last = _abi.TokenDesc(T, self.H, self.E, self.k, self._code)
-        return d
+        return _abi.TokenDesc(T, self.H, self.E, self.k, _abi.DTYPES[self.dtype])
 
-    def _rows(self, t: torch.Tensor, name: str, rows: int) -> None:
-        check_tensor(t, name, (rows, self.H), self.dtype, self.device)
-
-    def _table(self, t: torch.Tensor, name: str, dtype, T=None) -> int:
-        if T is None:
-            T = t.shape[0] if t.dim() == 2 else -1
-        check_tensor(t, name, (T, self.k), dtype, self.device)
-        return T
-
-    def _call(self, fn, *args, stream=None):
-        if torch.cuda.current_device() == self.device.index:
-            fn(*args, stream=stream)
-        else:
-            with torch.cuda.device(self.device):
-                fn(*args, stream=stream)
+    def _ref(self, T: int):
+        last = self._last
+        if last[0] != T:
+            last = self._last = (T, ctypes.byref(self._desc(T)))
+        return last[1]
 
     def sort(self, x: torch.Tensor, topk_idx: torch.Tensor, out=None, stream=None):
         """x [T, H], topk_idx [T, k] int32 -> (x_sorted [T*k, H], offsets [E+1], slot_of [T, k] int32)."""
-        T, dev = self._table(topk_idx, "topk_idx", torch.int32), self.device
+        T, H, k, dt, dev = x.shape[0], self.H, self.k, self.dtype, self._dev
+        check_tensor(x, "x", (T, H), dt, dev)
+        check_tensor(topk_idx, "topk_idx", (T, k), torch.int32, dev)
         if T > self.max_tokens:
             raise ValueError(f"{T} tokens exceed the workspace size of {self.max_tokens}")
-        self._rows(x, "x", T)
         if out is None:
-            out = (torch.empty((T * self.k, self.H), dtype=self.dtype, device=dev),
-                   torch.empty(self.E + 1, dtype=torch.int32, device=dev),
-                   torch.empty((T, self.k), dtype=torch.int32, device=dev))
+            out = (torch.empty((T * k, H), dtype=dt, device=self.device),
+                   torch.empty(self.E + 1, dtype=torch.int32, device=self.device),
+                   torch.empty((T, k), dtype=torch.int32, device=self.device))
         x_sorted, offsets, slot_of = out
-        self._rows(x_sorted, "x_sorted", T * self.k)
+        check_tensor(x_sorted, "x_sorted", (T * k, H), dt, dev)
         check_tensor(offsets, "offsets", (self.E + 1,), torch.int32, dev)
-        self._table(slot_of, "slot_of", torch.int32, T)
-        self._call(_abi.moe_sort_tokens, self._desc(T), x, topk_idx, x_sorted, offsets, slot_of, self.ws,
-                   stream=stream)
+        check_tensor(slot_of, "slot_of", (T, k), torch.int32, dev)
+        self._run(self._lib.moe_sort_tokens, stream, self._ref(T), x.data_ptr(), topk_idx.data_ptr(), x_sorted.data_ptr(),
+                  offsets.data_ptr(), slot_of.data_ptr(), self.ws.data_ptr(), self.ws.numel())
         return out
 
     def sort_backward(self, dx_sorted: torch.Tensor, slot_of: torch.Tensor, out=None, stream=None):
         """dx_sorted [T*k, H] -> dx [T, H], the sum of each token's rows."""
-        T = self._table(slot_of, "slot_of", torch.int32)
-        self._rows(dx_sorted, "dx_sorted", T * self.k)
+        T, H, dt, dev = slot_of.shape[0], self.H, self.dtype, self._dev
+        check_tensor(slot_of, "slot_of", (T, self.k), torch.int32, dev)
+        check_tensor(dx_sorted, "dx_sorted", (T * self.k, H), dt, dev)
         if out is None:
-            out = torch.empty((T, self.H), dtype=self.dtype, device=self.device)
-        self._rows(out, "dx", T)
-        self._call(_abi.moe_sort_tokens_backward, self._desc(T), dx_sorted, slot_of, out, stream=stream)
+            out = torch.empty((T, H), dtype=dt, device=self.device)
+        check_tensor(out, "dx", (T, H), dt, dev)
+        self._run(self._lib.moe_sort_tokens_backward, stream, self._ref(T), dx_sorted.data_ptr(), slot_of.data_ptr(),
+                  out.data_ptr())
         return out
 
     def unsort(self, y_sorted: torch.Tensor, slot_of: torch.Tensor, topk_w=None, add=None, out=None, stream=None):
         """y_sorted [T*k, H] -> y [T, H]: each token's rows weighted by topk_w [T, k] fp32 (None: 1)
         and summed, plus add [T, H] (None: 0)."""
-        T = self._table(slot_of, "slot_of", torch.int32)
-        self._rows(y_sorted, "y_sorted", T * self.k)
+        T, H, dt, dev = slot_of.shape[0], self.H, self.dtype, self._dev
+        check_tensor(slot_of, "slot_of", (T, self.k), torch.int32, dev)
+        check_tensor(y_sorted, "y_sorted", (T * self.k, H), dt, dev)
         if topk_w is not None:
-            self._table(topk_w, "topk_w", torch.float32, T)
+            check_tensor(topk_w, "topk_w", (T, self.k), torch.float32, dev)
         if add is not None:
-            self._rows(add, "add", T)
+            check_tensor(add, "add", (T, H), dt, dev)
         if out is None:
-            out = torch.empty((T, self.H), dtype=self.dtype, device=self.device)
-        self._rows(out, "y", T)
-        self._call(_abi.moe_unsort_tokens, self._desc(T), y_sorted, slot_of, topk_w, add, out, stream=stream)
+            out = torch.empty((T, H), dtype=dt, device=self.device)
+        check_tensor(out, "y", (T, H), dt, dev)
+        self._run(self._lib.moe_unsort_tokens, stream, self._ref(T), y_sorted.data_ptr(), slot_of.data_ptr(),
+                  None if topk_w is None else topk_w.data_ptr(), None if add is None else add.data_ptr(), out.data_ptr())
         return out
 
     def unsort_backward(self, dy: torch.Tensor, y_sorted: torch.Tensor, slot_of: torch.Tensor, topk_w=None, out=None,
                         stream=None):
         """dy [T, H] -> (dy_sorted [T*k, H], dtopk_w [T, k] fp32). The gradient of unsort's `add` is dy."""
-        T = self._table(slot_of, "slot_of", torch.int32)
-        self._rows(dy, "dy", T)
-        self._rows(y_sorted, "y_sorted", T * self.k)
+        T, H, k, dt, dev = slot_of.shape[0], self.H, self.k, self.dtype, self._dev
+        check_tensor(slot_of, "slot_of", (T, k), torch.int32, dev)
+        check_tensor(dy, "dy", (T, H), dt, dev)
+        check_tensor(y_sorted, "y_sorted", (T * k, H), dt, dev)
         if topk_w is not None:
-            self._table(topk_w, "topk_w", torch.float32, T)
+            check_tensor(topk_w, "topk_w", (T, k), torch.float32, dev)
         if out is None:
-            out = (torch.empty((T * self.k, self.H), dtype=self.dtype, device=self.device),
-                   torch.empty((T, self.k), dtype=torch.float32, device=self.device))
+            out = (torch.empty((T * k, H), dtype=dt, device=self.device),
+                   torch.empty((T, k), dtype=torch.float32, device=self.device))
         dy_sorted, dtopk_w = out
-        self._rows(dy_sorted, "dy_sorted", T * self.k)
-        self._table(dtopk_w, "dtopk_w", torch.float32, T)
-        self._call(_abi.moe_unsort_tokens_backward, self._desc(T), dy, y_sorted, slot_of, topk_w, dy_sorted, dtopk_w,
-                   stream=stream)
+        check_tensor(dy_sorted, "dy_sorted", (T * k, H), dt, dev)
+        check_tensor(dtopk_w, "dtopk_w", (T, k), torch.float32, dev)
+        self._run(self._lib.moe_unsort_tokens_backward, stream, self._ref(T), dy.data_ptr(), y_sorted.data_ptr(),
+                  slot_of.data_ptr(), None if topk_w is None else topk_w.data_ptr(), dy_sorted.data_ptr(),
+                  dtopk_w.data_ptr())
         return out
