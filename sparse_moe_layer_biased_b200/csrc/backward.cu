@@ -515,6 +515,12 @@ __device__ __forceinline__ void bwd_epilogue(const BwdArgs &a, uint32_t tacc, co
                 }
             }
         }
+        // the group's padding rows (behind its last chunk): WD multiplies them with dy_pad's zeros,
+        // and a NaN that the workspace held before would pass through
+        if (!is_up)
+            for (int64_t r = t.row0 + t.ntok; r & (kBwdPad - 1); ++r)
+                if (a.tok_pad[r] < 0)
+                    hw[(r - t.row0 + rs) * Iw + f] = 0;
     } else if (MODE == kBwdDH) {
         // blocks of 16 columns; the two warps of a lane quarter take alternate blocks
         const int64_t i = t.mb * 128 + row;
@@ -582,6 +588,13 @@ __device__ __forceinline__ void bwd_epilogue(const BwdArgs &a, uint32_t tacc, co
                 __syncwarp();
             }
         }
+        // padding rows as in GU (WGU multiplies them with x_pad's zeros)
+        if (half == 0)
+            for (int64_t r = t.row0 + t.ntok; r & (kBwdPad - 1); ++r)
+                if (a.tok_pad[r] < 0) {
+                    dgu[(r - t.row0 + rs) * 2 * Iw + i] = 0;
+                    dgu[(r - t.row0 + rs) * 2 * Iw + Iw + i] = 0;
+                }
     } else if (MODE == kBwdDX) {
         const int64_t h = t.mb * 128 + row;
         for (int cb = 0; cb < t.ntok; cb += 32) {
