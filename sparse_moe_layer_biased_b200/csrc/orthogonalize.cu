@@ -648,15 +648,15 @@ __global__ void __launch_bounds__(OrthGeo<PAIR>::kThreads, 1)
             }
             // The loads this CTA issued must have landed before it leaves. The leader's barriers
             // count both CTAs' bytes; the peer, which cannot wait on them, leaves behind the final
-            // cluster barrier, and after an abort (when it may have issued stages that the leader never
-            // armed) waits 200 us first, far longer than a load takes.
-            if (rank == 0) {
-                for (int i = it > S ? it - S : 0; i < it; ++i)
-                    mbar_wait_drain(&full[i % S], (i / S) & 1, wc);
-            } else if (stop || *abort_flag) {
+            // cluster barrier. After an abort either may have issued stages that the other did not,
+            // whose barriers never complete: both then wait 200 us, far longer than a load takes.
+            if (PAIR && (stop || *abort_flag)) {
                 const unsigned long long t0 = global_ns();
                 while (global_ns() - t0 < 200000ull) {
                 }
+            } else if (rank == 0) {
+                for (int i = it > S ? it - S : 0; i < it; ++i)
+                    mbar_wait_drain(&full[i % S], (i / S) & 1, wc);
             }
         }
     } else if (warp == 1) {

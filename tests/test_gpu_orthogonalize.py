@@ -123,28 +123,30 @@ def test_result_is_nearly_orthogonal():
     assert 0.68 - slack <= s.min().item() and s.max().item() <= 1.21 + slack
 
 
-def test_zero_tiny_huge_and_broken_matrices():
+@pytest.mark.parametrize("rows,cols", [(72, 200), (150, 216), (330, 150)])
+def test_zero_tiny_huge_and_broken_matrices(rows, cols):
     """Each matrix by itself: a zero one gives zero, sizes of 1e-30 and 1e30 change nothing but by eps, a NaN or
     an infinity spoils its own matrix only."""
-    g = gauss(7, 72, 200, 10)
+    g = gauss(7, rows, cols, 10)
     g[0] = 0
     g[2] *= 1e30
     g[3, 5, 6] = float("nan")
     g[4, 1, 2] = float("inf")
     g[6] *= 1e-30
-    out = moe.Orthogonalizer(7, 72, 200, eps=1e-36).orthogonalize(g)
+    out = moe.Orthogonalizer(7, rows, cols, eps=1e-36).orthogonalize(g)
     assert bool((out[0] == 0).all())
     assert bool(torch.isnan(out[3]).all()) and bool(torch.isnan(out[4]).all())
     ok = [1, 2, 5, 6]
     check(out[ok], reference(g[ok], eps=1e-36))
     # eps counts against the norm
-    g = gauss(1, 72, 200, 11) * 1e-9
-    check(moe.Orthogonalizer(1, 72, 200, eps=1e-7).orthogonalize(g), reference(g, eps=1e-7))
+    g = gauss(1, rows, cols, 11) * 1e-9
+    check(moe.Orthogonalizer(1, rows, cols, eps=1e-7).orthogonalize(g), reference(g, eps=1e-7))
 
 
-def test_same_bits_on_a_side_stream_and_from_a_graph():
-    o = moe.Orthogonalizer(5, 136, 264)
-    g, m = gauss(5, 136, 264, 12), gauss(5, 136, 264, 13)
+@pytest.mark.parametrize("rows,cols", [(136, 264), (40, 700), (900, 520)])
+def test_same_bits_on_a_side_stream_and_from_a_graph(rows, cols):
+    o = moe.Orthogonalizer(5, rows, cols)
+    g, m = gauss(5, rows, cols, 12), gauss(5, rows, cols, 13)
     want = o.orthogonalize(g, momentum=m.clone()).clone()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
