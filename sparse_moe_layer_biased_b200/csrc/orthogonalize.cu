@@ -233,17 +233,21 @@ template <typename G, bool kVec>
 __global__ void __launch_bounds__(256)
     orth_cast_kernel(const PrepArgs a)
 {
-    __shared__ double inv_s;
+    __shared__ double warp_sum[8];
     allow_dependents();
     dependency_wait();
-    if (threadIdx.x == 0) {
-        double s = 0.0;
-        for (int i = 0; i < a.parts; ++i)
-            s += a.part[static_cast<int64_t>(blockIdx.y) * a.parts + i];
-        inv_s = static_cast<double>(kSx) / (sqrt(s) + a.eps);
-    }
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < a.parts; i += 256)
+        sum += a.part[static_cast<int64_t>(blockIdx.y) * a.parts + i];
+    for (int o = 16; o > 0; o >>= 1)
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if ((threadIdx.x & 31) == 0)
+        warp_sum[threadIdx.x >> 5] = sum;
     __syncthreads();
-    const Scale scale(inv_s);
+    sum = 0.0;
+    for (int w = 0; w < 8; ++w)
+        sum += warp_sum[w];
+    const Scale scale(static_cast<double>(kSx) / (sqrt(sum) + a.eps));
     const int64_t base = static_cast<int64_t>(blockIdx.y) * a.rows * a.cols;
     const G *g = static_cast<const G *>(a.grad) + base;
     const float *m = a.momentum ? a.momentum + base : nullptr;
@@ -1400,8 +1404,8 @@ OrthLayout orth_layout(const moe_orthogonalize_desc &d)
     L.a_mat = L.p * L.a_pitch;
     L.r_mat = up(L.p, 64);
     const size_t elems = rows * cols;
-    const size_t parts = (elems + 16383) / 16384;  // 64 elements a thread
-    L.parts = static_cast<int>(parts < 1 ? 1 : (parts > 64 ? 64 : parts));
+    const size_t parts = (elems + 8191) / 8192;  // 32 elements a thread, or more
+    L.parts = static_cast<int>(parts > 512 ? 512 : parts);
     const size_t each = 6 * L.x_mat + 6 * L.a_mat + 8 * L.r_mat + 8 * L.parts;
     size_t most = kChunkBytes / each;
     most = most < 1 ? 1 : most;
