@@ -1441,16 +1441,30 @@ bool iterates_fit(const moe_orthogonalize_desc &d)
     for (int s = 0; s < d.steps; ++s) {
         if (!(top <= 7.9) || !(top * top <= 31.0))
             return false;
-        double next = 0.0, bmax = 0.0;
-        constexpr int kPoints = 4096;
-        for (int i = 0; i <= kPoints; ++i) {
-            const double x = top * i / kPoints, l = x * x;
-            const double bb = std::fabs(b * l + c * l * l), px = std::fabs(x * (a + b * l + c * l * l));
-            next = px > next ? px : next;
-            bmax = bb > bmax ? bb : bmax;
-        }
+        const double l = top * top;  // eigenvalues of A lie in [0, l]
+        // |b t + c t^2| is largest at l or at its vertex
+        const auto bt = [&](double t) { return std::fabs(t * (b + c * t)); };
+        double bmax = bt(l);
+        if (c != 0.0 && -b / (2.0 * c) > 0.0 && -b / (2.0 * c) < l)
+            bmax = std::fmax(bmax, bt(-b / (2.0 * c)));
         if (!(bmax <= 31.0))
             return false;
+        // |x (a + b x^2 + c x^4)| at top or where 5 c t^2 + 3 b t + a = 0, t = x^2
+        const auto px = [&](double t) { return std::fabs(std::sqrt(t) * (a + t * (b + c * t))); };
+        double next = px(l);
+        double roots[2] = {-1.0, -1.0};
+        if (c != 0.0) {
+            const double disc = 9.0 * b * b - 20.0 * a * c;
+            if (disc >= 0.0) {
+                roots[0] = (-3.0 * b + std::sqrt(disc)) / (10.0 * c);
+                roots[1] = (-3.0 * b - std::sqrt(disc)) / (10.0 * c);
+            }
+        } else if (b != 0.0) {
+            roots[0] = -a / (3.0 * b);
+        }
+        for (double t : roots)
+            if (t > 0.0 && t < l)
+                next = std::fmax(next, px(t));
         top = 1.01 * next;
     }
     return std::isfinite(top);
