@@ -17,6 +17,7 @@
 // bandwidth bounds the large calls, launch and dependent-load latency the small ones. Sums
 // run in fp32, over j in rank order, and round once to the rows' type.
 #include <atomic>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -44,10 +45,10 @@ __device__ __forceinline__ int entry_key(int id, int n, int E, int N)
     return static_cast<unsigned>(id) < static_cast<unsigned>(E) ? id * N + n : kDroppedKey;
 }
 
-// A row (units of U) to the rows slots[0..k) of x_sorted, columns [c0, c1). Every load of a piece
+// A row (units of U) to the rows slots[0..k) of x_sorted, up to column c1, by LANES threads. Every load of a piece
 // (V units per thread) is issued before its k copies are stored; load() may run before the
 // slots are known.
-template <typename U>
+template <typename U, int LANES>
 struct RowCopy {
     static constexpr int V = sizeof(U) >= 8 ? 4 : 8;
     U v[V];
@@ -55,8 +56,8 @@ struct RowCopy {
     {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (c + i * kRowThreads < c1)
-                v[i] = src[c + i * kRowThreads];
+            if (c + i * LANES < c1)
+                v[i] = src[c + i * LANES];
     }
     __device__ __forceinline__ void store(U *__restrict__ out, int64_t units, int64_t c, int64_t c1, const int *slots,
                                           int k) const
@@ -68,8 +69,8 @@ struct RowCopy {
             U *dst = out + s * units;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (c + i * kRowThreads < c1)
-                    dst[c + i * kRowThreads] = v[i];
+                if (c + i * LANES < c1)
+                    dst[c + i * LANES] = v[i];
         }
     }
 };
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(kRowThreads)
     const U *src = x + static_cast<int64_t>(t) * units;
     const int64_t c1 = (blockIdx.y + 1) * chunk < units ? (blockIdx.y + 1) * chunk : units;
     int64_t c = blockIdx.y * chunk + threadIdx.x;
-    RowCopy<U> row;
+    RowCopy<U, kRowThreads> row;
     row.load(src, c, c1);  // on its way while the places are counted
     for (int n = threadIdx.x; n < N; n += kRowThreads)
         tab[n] = entry_key(idx[n], n, E, N);
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kRowThreads)
     }
     for (;;) {
         row.store(x_sorted, units, c, c1, slots, k);
-        c += RowCopy<U>::V * kRowThreads;
+        c += RowCopy<U, kRowThreads>::V * kRowThreads;
         if (c >= c1)
             break;
         row.load(src, c, c1);
@@ -321,6 +322,7 @@ constexpr int kCountThreads = 256;
 constexpr int kCountWarps = kCountThreads / 32;
 constexpr int kCountBlocks = 128;  // most blocks of the count
 constexpr int kScanCtas = 8;
+constexpr int kScanGroups = 32;  // most parts of the blocks that are summed side by side
 
 __global__ void __launch_bounds__(kCountThreads)
     sort_count_kernel(const int32_t *__restrict__ idx, int64_t N, int E, int per, int32_t *__restrict__ hist,
@@ -379,10 +381,10 @@ __global__ void __launch_bounds__(1024)
     __shared__ int cta_total;
     allow_dependents();
     dependency_wait();
-    const int groups = 1024 / ep_pad;
+    const int groups = 1024 / ep_pad < kScanGroups ? 1024 / ep_pad : kScanGroups;  // threads beyond idle
     const int le = threadIdx.x % ep_pad, g = threadIdx.x / ep_pad;
     const int e = static_cast<int>(cluster_ctarank()) * ep + le;
-    const bool on = le < ep && e < E;
+    const bool on = le < ep && e < E && g < groups;
     const int span = (nb + groups - 1) / groups;
     const int b0 = g * span < nb ? g * span : nb, b1 = b0 + span < nb ? b0 + span : nb;
     int sum = 0;
@@ -439,24 +441,29 @@ __global__ void __launch_bounds__(1024)
     cluster_sync_all();  // no CTA leaves while a peer may still read its total
 }
 
-// Block t copies token t's row; its loads are on their way before the places are. kFinal: slot_of
-// holds the places already (sort_places_kernel). What the launch before wrote is read through
-// pointers without __restrict__: such loads could move above the wait.
-template <typename U, bool kFinal>
+// Blocks copy the rows of kRowThreads / LANES tokens each; their loads are on their way before the places
+// are. kFinal: slot_of holds the places already (sort_places_kernel). What the launch before wrote is read
+// through pointers without __restrict__: such loads could move above the wait.
+template <typename U, bool kFinal, int LANES>
 __global__ void __launch_bounds__(kRowThreads)
-    sort_rows_kernel(const U *__restrict__ x, const int32_t *__restrict__ idx, int k, int E, int per,
+    sort_rows_kernel(const U *__restrict__ x, const int32_t *__restrict__ idx, int T, int k, int E, int per,
                      const int32_t *hist, const int32_t *rank, int64_t units, U *__restrict__ x_sorted,
                      int32_t *slot_of)
 {
-    __shared__ int slots[kMaxK];
-    const int64_t t = blockIdx.x;
+    constexpr int kTokens = kRowThreads / LANES;
+    __shared__ int slots[kMaxK * kTokens];
+    const int mine = threadIdx.x / LANES;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens, t = t0 + mine;
     const U *src = x + t * units;
-    int64_t c = threadIdx.x;
-    RowCopy<U> row;
-    row.load(src, c, units);
+    int64_t c = threadIdx.x % LANES;
+    const int64_t end = t < T ? units : 0;
+    RowCopy<U, LANES> row;
+    row.load(src, c, end);
     dependency_wait();
-    if (threadIdx.x < k) {
-        const int64_t n = t * k + threadIdx.x;
+    const int64_t n0 = t0 * k;
+    const int count = static_cast<int>(T - t0 < kTokens ? T - t0 : kTokens) * k;
+    for (int i = threadIdx.x; i < count; i += kRowThreads) {
+        const int64_t n = n0 + i;
         int s;
         if (kFinal) {
             s = slot_of[n];
@@ -465,16 +472,31 @@ __global__ void __launch_bounds__(kRowThreads)
             s = r < 0 ? -1 : hist[n / per * E + idx[n]] + r;
             slot_of[n] = s;
         }
-        slots[threadIdx.x] = s;
+        slots[i] = s;
     }
     __syncthreads();
-    for (;;) {
-        row.store(x_sorted, units, c, units, slots, k);
-        c += RowCopy<U>::V * kRowThreads;
-        if (c >= units)
-            break;
-        row.load(src, c, units);
+    while (c < end) {
+        row.store(x_sorted, units, c, end, slots + mine * k, k);
+        c += RowCopy<U, LANES>::V * LANES;
+        if (c < end)
+            row.load(src, c, end);
     }
+}
+
+// Rows of up to 8 units share a block of 16 tokens, rows that a warp holds at once one of 4: 8000 rows of 128
+// bytes copied to 8 places each 13 us, 26 us with a block per row; 20000 of 180 bytes to 4 places 20 for 33 us; 16000 of 528
+// bytes to 2 places 9.7 for 15 us; 4000 of 1040 bytes 6.1 for 6.7 us.
+template <typename U, bool kFinal>
+cudaError_t launch_rows(const U *x, const int32_t *idx, int T, int k, int E, int per, const int32_t *hist,
+                        const int32_t *rank, int64_t units, U *x_sorted, int32_t *slot_of, cudaStream_t stream)
+{
+    const int lanes = units <= 8 ? 8 : (units <= 32 * RowCopy<U, 32>::V ? 32 : kRowThreads);
+    auto kernel = lanes == 8    ? sort_rows_kernel<U, kFinal, 8>
+                  : lanes == 32 ? sort_rows_kernel<U, kFinal, 32>
+                                : sort_rows_kernel<U, kFinal, kRowThreads>;
+    const int tokens = kRowThreads / lanes;
+    return launch_dependent(kernel, dim3((T + tokens - 1) / tokens), kRowThreads, 0, stream, 1, x, idx, T, k, E, per,
+                            hist, rank, units, x_sorted, slot_of);
 }
 
 struct SortPlan {
@@ -551,9 +573,7 @@ cudaError_t launch_sort(const void *x, const int32_t *idx, int T, int k, int E, 
         cudaError_t err = launch_places(idx, static_cast<int>(N), E, offsets, slot_of, stream);
         if (err != cudaSuccess)
             return err;
-        return launch_dependent(sort_rows_kernel<U, true>, dim3(T), kRowThreads, 0, stream, 1, xs, idx, k, E, 1,
-                                static_cast<const int32_t *>(nullptr), static_cast<const int32_t *>(nullptr), units,
-                                out, slot_of);
+        return launch_rows<U, true>(xs, idx, T, k, E, 1, nullptr, nullptr, units, out, slot_of, stream);
     }
     const SortPlan p = sort_plan(N, E);
     int32_t *hist = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + p.hist);
@@ -570,9 +590,7 @@ cudaError_t launch_sort(const void *x, const int32_t *idx, int T, int k, int E, 
                            offsets);
     if (err != cudaSuccess)
         return err;
-    return launch_dependent(sort_rows_kernel<U, false>, dim3(T), kRowThreads, 0, stream, 1, xs, idx, k, E, p.per,
-                            static_cast<const int32_t *>(hist), static_cast<const int32_t *>(rank), units, out,
-                            slot_of);
+    return launch_rows<U, false>(xs, idx, T, k, E, p.per, hist, rank, units, out, slot_of, stream);
 }
 
 // --------------------------------------------------------------------- rows in fp32 and back
@@ -593,24 +611,60 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// y[t] = add[t] + sum_j w[t, j] rows[slot_of[t, j]] (w NULL: 1, add NULL: 0) for packs [c0, c0 +
-// chunk) of the row; a slot outside [0, N) contributes nothing. The chunks of a token are
-// neighbours in the grid, so that a row's 8 KB are read at one time: with the tokens innermost DRAM saw
-// 2 KB pieces: 4.8 against 6.6 TB/s over 1.2 GB. kOne: k <= 8, slots and weights stay in registers.
-template <typename S, int VEC, bool kOne>
-__global__ void __launch_bounds__(kRowThreads)
+// p = *src where `on`; p is undefined elsewhere. One predicated load: as a branch around it, the loads of a batch
+// wait for one another.
+template <typename P>
+__device__ __forceinline__ void load_if(P &p, const P *src, bool on)
+{
+    static_assert(sizeof(P) == 2 || sizeof(P) == 4 || sizeof(P) == 8 || sizeof(P) == 16, "pack");
+    const int q = on;
+    if constexpr (sizeof(P) == 16) {
+        uint4 u;
+        asm("{\n.reg .pred q;\nsetp.ne.b32 q, %5, 0;\n@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+            : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+            : "l"(src), "r"(q));
+        memcpy(&p, &u, sizeof(P));
+    } else if constexpr (sizeof(P) == 8) {
+        uint2 u;
+        asm("{\n.reg .pred q;\nsetp.ne.b32 q, %3, 0;\n@q ld.global.nc.v2.u32 {%0, %1}, [%2];\n}"
+            : "=r"(u.x), "=r"(u.y)
+            : "l"(src), "r"(q));
+        memcpy(&p, &u, sizeof(P));
+    } else if constexpr (sizeof(P) == 4) {
+        uint32_t u;
+        asm("{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n@q ld.global.nc.u32 %0, [%1];\n}" : "=r"(u) : "l"(src), "r"(q));
+        memcpy(&p, &u, sizeof(P));
+    } else {
+        uint16_t u;
+        asm("{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n@q ld.global.nc.u16 %0, [%1];\n}" : "=h"(u) : "l"(src), "r"(q));
+        memcpy(&p, &u, sizeof(P));
+    }
+}
+
+// y[t] = add[t] + sum_j w[t, j] rows[slot_of[t, j]] (w NULL: 1, add NULL: 0) by LANES threads per token
+// for packs [c0, c0 + chunk) of the row; a slot outside [0, N) contributes nothing. The chunks of a
+// token are neighbours in the grid, so that a row's 8 KB are read at one time: with the tokens
+// innermost DRAM saw 2 KB pieces, 4.8 against 6.6 TB/s over 1.2 GB. K: the most slots (4 or 8), which stay in registers
+// with their weights; 0: any number, eight at a time. Narrow packs (rows that are not 16-byte aligned) go four at a time, for as many bytes in flight.
+template <typename S, int VEC, int K, int LANES, int THREADS>
+__global__ void __launch_bounds__(THREADS)
     unsort_kernel(const S *__restrict__ rows, const int32_t *__restrict__ slot_of, const float *__restrict__ w,
-                  const S *__restrict__ add, int k, int64_t N, int H, int chunk, int chunks, S *__restrict__ y)
+                  const S *__restrict__ add, int T, int k, int64_t N, int H, int chunk, int chunks, S *__restrict__ y)
 {
     using P = Pack<S, VEC>;
-    const int64_t t = blockIdx.x / chunks;
-    const int c0 = (blockIdx.x - static_cast<int>(t) * chunks) * chunk;
+    constexpr int KB = K ? K : 8;
+    constexpr int NV = sizeof(P) <= 4 ? 4 : 1;
+    const int group = blockIdx.x / chunks;  // of THREADS / LANES tokens
+    const int64_t t = static_cast<int64_t>(group) * (THREADS / LANES) + threadIdx.x / LANES;
+    if (t >= T)
+        return;
+    const int c0 = (blockIdx.x - group * chunks) * chunk;
     const int c1 = c0 + chunk < H / VEC ? c0 + chunk : H / VEC;
-    int s[8];
-    float wj[8];
+    int s[KB];
+    float wj[KB];
     auto fetch = [&](int j0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < KB; ++j) {
             s[j] = -1;
             wj[j] = 1.0f;
             if (j0 + j < k) {
@@ -622,54 +676,65 @@ __global__ void __launch_bounds__(kRowThreads)
             }
         }
     };
-    if (kOne)
+    if (K)
         fetch(0);
-    for (int c = c0 + threadIdx.x; c < c1; c += kRowThreads) {
-        const int64_t col = static_cast<int64_t>(c) * VEC;
-        P a;
-        if (add)
-            a = *reinterpret_cast<const P *>(add + t * H + col);
-        float acc[VEC];
+    for (int c = c0 + threadIdx.x % LANES; c < c1; c += NV * LANES) {
+        P a[NV];
+        float acc[NV][VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            acc[i] = 0.0f;
-        for (int j0 = 0; j0 < k; j0 += 8) {
-            if (!kOne)
-                fetch(j0);
-            P r[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (s[j] >= 0)
-                    r[j] = *reinterpret_cast<const P *>(rows + static_cast<int64_t>(s[j]) * H + col);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (s[j] >= 0)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        acc[i] = fmaf(wj[j], to_f32(r[j].v[i]), acc[i]);
-            if (kOne)
-                break;
-        }
-        if (add)
+        for (int v = 0; v < NV; ++v) {
+            if (add && (NV == 1 || c + v * LANES < c1))
+                a[v] = *reinterpret_cast<const P *>(add + t * H + static_cast<int64_t>(c + v * LANES) * VEC);
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                acc[i] += to_f32(a.v[i]);
-        P o;
+                acc[v][i] = 0.0f;
+        }
+        for (int j0 = 0; j0 < k; j0 += KB) {
+            if (!K)
+                fetch(j0);
+            P r[KB][NV];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            o.v[i] = from_f32<S>(acc[i]);
-        *reinterpret_cast<P *>(y + t * H + col) = o;
+            for (int j = 0; j < KB; ++j)
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+                    load_if(r[j][v],
+                            reinterpret_cast<const P *>(rows + static_cast<int64_t>(s[j]) * H +
+                                                        static_cast<int64_t>(c + v * LANES) * VEC),
+                            s[j] >= 0 && (NV == 1 || c + v * LANES < c1));
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+                if (s[j] >= 0)
+#pragma unroll
+                    for (int v = 0; v < NV; ++v)
+                        if (NV == 1 || c + v * LANES < c1)
+#pragma unroll
+                            for (int i = 0; i < VEC; ++i)
+                                acc[v][i] = fmaf(wj[j], to_f32(r[j][v].v[i]), acc[v][i]);
+            if (K)
+                break;
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            if (NV > 1 && c + v * LANES >= c1)
+                break;
+            P o;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                o.v[i] = from_f32<S>(add ? acc[v][i] + to_f32(a[v].v[i]) : acc[v][i]);
+            *reinterpret_cast<P *>(y + t * H + static_cast<int64_t>(c + v * LANES) * VEC) = o;
+        }
     }
 }
 
 // The gradient of the unsort: per entry its row of dy_sorted and, through a sum in a fixed order,
-// its dw. Many entries of narrow rows: a warp per entry, the entries of a token in one block or
-// neighbouring ones, so that dy comes from L1 for all but the first; no barrier, U packs of both
-// rows in flight per lane. Against the blocks below: 4500 entries of 4092 bytes 8.1 against 17 us; 32768 entries
-// of 8 KB 109 against 99 us.
+// its dw. LANES threads per entry, the entries of a token in one block or neighbouring ones, so that dy
+// comes from L1 for all but the first; no barrier, U packs of both rows in flight per lane (of 16-byte packs four:
+// 53175 entries of 2128 bytes take 49 us, with two 46, with eight 74; 8000 of 16 KB 48, 54 and 51). A warp
+// for 32768 entries of 8 KB: 89 us, 6.4 TB/s. Eight lanes for rows of up to 8 packs: 64000 entries of 128 bytes 6 us,
+// a warp for each 18 us.
 constexpr int kBackThreads = 256;
 
-template <typename S, int VEC>
+template <typename S, int VEC, int LANES>
 __global__ void __launch_bounds__(kBackThreads)
     unsort_backward_kernel(const S *__restrict__ dy, const S *__restrict__ rows, const int32_t *__restrict__ slot_of,
                            const float *__restrict__ w, int k, int64_t N, int H, S *__restrict__ drows,
@@ -677,11 +742,10 @@ __global__ void __launch_bounds__(kBackThreads)
 {
     using P = Pack<S, VEC>;
     constexpr int U = sizeof(P) >= 16 ? 4 : 8;
-    const int lane = threadIdx.x & 31;
-    const int64_t n = static_cast<int64_t>(blockIdx.x) * (kBackThreads / 32) + (threadIdx.x >> 5);
-    if (n >= N)
-        return;
-    const int64_t s = slot_of[n];
+    const int lane = threadIdx.x % LANES;
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * (kBackThreads / LANES) + threadIdx.x / LANES;
+    const bool on = n < N;  // lanes without an entry stay for the others' sums
+    const int64_t s = on ? slot_of[n] : -1;
     float acc = 0.0f;
     if (s >= 0 && s < N) {
         const float wn = w ? w[n] : 1.0f;
@@ -690,18 +754,16 @@ __global__ void __launch_bounds__(kBackThreads)
         const P *r_row = reinterpret_cast<const P *>(rows + s * H);
         P *d_row = reinterpret_cast<P *>(drows + s * H);
         const int packs = H / VEC;
-        for (int c = lane; c < packs; c += U * 32) {
+        for (int c = lane; c < packs; c += U * LANES) {
             P g[U], r[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (c + u * 32 < packs) {
-                    g[u] = g_row[c + u * 32];
-                    if (dw)
-                        r[u] = r_row[c + u * 32];
-                }
+            for (int u = 0; u < U; ++u) {
+                load_if(g[u], g_row + c + u * LANES, c + u * LANES < packs);
+                load_if(r[u], r_row + c + u * LANES, dw && c + u * LANES < packs);
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (c + u * 32 < packs) {
+                if (c + u * LANES < packs) {
                     if (dw)
 #pragma unroll
                         for (int i = 0; i < VEC; ++i)
@@ -711,31 +773,30 @@ __global__ void __launch_bounds__(kBackThreads)
 #pragma unroll
                         for (int i = 0; i < VEC; ++i)
                             o.v[i] = from_f32<S>(wn * to_f32(g[u].v[i]));
-                        d_row[c + u * 32] = o;
+                        d_row[c + u * LANES] = o;
                     }
                 }
         }
     }
     if (!dw)
         return;
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = LANES / 2; o > 0; o >>= 1)
         acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
-    if (lane == 0)
+    if (on && lane == 0)
         dw[n] = acc;
 }
 
-// JB entries of one token per block. Eight for wide rows of many tokens: 4 KB of dy, then 4 KB
-// of up to eight rows at a time, longer runs of reads and of writes in DRAM than from a warp per
-// entry. One for few entries, so that they fill the SMs (dy is then read k times): 512 entries 3.2 us, a warp
-// per entry or eight entries per block 4.5 us and more.
-template <typename S, int VEC, int JB>
-__global__ void __launch_bounds__(kBackThreads)
+// JB entries of one token per block. Four or eight for rows of 9 to 64 packs and many tokens: 32000 entries of
+// 528 bytes 13 us, a warp for each 18 us; for 32768 of 8 KB 99 against 89 us. One for few entries, so that they fill
+// the SMs (dy is then read k times): 512 entries 3.2 us, a warp per entry or eight entries per block 4.5 us and more.
+template <typename S, int VEC, int JB, int THREADS>
+__global__ void __launch_bounds__(THREADS)
     unsort_backward_token_kernel(const S *__restrict__ dy, const S *__restrict__ rows,
                                  const int32_t *__restrict__ slot_of, const float *__restrict__ w, int k, int64_t N,
                                  int H, S *__restrict__ drows, float *__restrict__ dw)
 {
     using P = Pack<S, VEC>;
-    __shared__ float part[kBackThreads / 32][JB];
+    __shared__ float part[THREADS / 32][JB];
     const int64_t t = blockIdx.x;
     const int j0 = blockIdx.y * JB;
     int s[JB];
@@ -753,14 +814,13 @@ __global__ void __launch_bounds__(kBackThreads)
                 s[j] = -1;
         }
     }
-    for (int col = threadIdx.x * VEC; col < H; col += kBackThreads * VEC) {
+    for (int col = threadIdx.x * VEC; col < H; col += THREADS * VEC) {
         const P g = *reinterpret_cast<const P *>(dy + t * H + col);
         P r[JB];
         if (dw) {
 #pragma unroll
             for (int j = 0; j < JB; ++j)
-                if (s[j] >= 0)
-                    r[j] = *reinterpret_cast<const P *>(rows + static_cast<int64_t>(s[j]) * H + col);
+                load_if(r[j], reinterpret_cast<const P *>(rows + static_cast<int64_t>(s[j]) * H + col), s[j] >= 0);
 #pragma unroll
             for (int j = 0; j < JB; ++j)
                 if (s[j] >= 0)
@@ -793,7 +853,7 @@ __global__ void __launch_bounds__(kBackThreads)
     __syncthreads();
     if (threadIdx.x < JB && j0 + static_cast<int>(threadIdx.x) < k) {
         float sum = 0.0f;
-        for (int i = 0; i < kBackThreads / 32; ++i)
+        for (int i = 0; i < THREADS / 32; ++i)
             sum += part[i][threadIdx.x];
         dw[t * k + j0 + threadIdx.x] = sum;
     }
@@ -813,26 +873,43 @@ int pack_bytes(int64_t row_bytes, int elem, std::initializer_list<const void *> 
 
 // Packs of a row per block and blocks per row: whole rows, but for few tokens as many pieces of at
 // least one pack per thread as give every SM sixteen blocks.
-void split_row(int64_t packs, int T, int num_sms, int &chunk, int &chunks)
+void split_row(int64_t packs, int T, int num_sms, int threads, int &chunk, int &chunks)
 {
     int64_t pieces = (16 * static_cast<int64_t>(num_sms) + T - 1) / T;
-    const int64_t most = (packs + kRowThreads - 1) / kRowThreads;
+    const int64_t most = (packs + threads - 1) / threads;
     pieces = pieces < most ? pieces : most;
     chunk = static_cast<int>(((packs + pieces - 1) / pieces + 31) / 32 * 32);
     chunks = static_cast<int>((packs + chunk - 1) / chunk);
 }
 
+// Rows of up to 8 packs share a block of 16 tokens, up to 64 one of 4, and up to 160 too where there are
+// tokens for every SM: 8000 tokens x 8 rows of 128 bytes 3.1 us, 128 threads a row 12.7; 4000 x 8 of 528 bytes 5.4 for
+// 7.7 us; 10635 x 5 of 2128 bytes 31 for 35 us, but 500 x 4 of them 3.8 for 2.6 us.
 template <typename S, int VEC>
 cudaError_t unsort_vec(const void *rows, const int32_t *slot_of, const float *w, const void *add, int T, int k, int H,
                        void *y, int num_sms, cudaStream_t stream)
 {
-    int chunk, chunks;
-    split_row(H / VEC, T, num_sms, chunk, chunks);
-    auto kernel = k <= 8 ? unsort_kernel<S, VEC, true> : unsort_kernel<S, VEC, false>;
-    kernel<<<static_cast<unsigned>(static_cast<int64_t>(T) * chunks), kRowThreads, 0, stream>>>(
-        static_cast<const S *>(rows), slot_of, w, static_cast<const S *>(add), k, static_cast<int64_t>(T) * k, H,
-        chunk, chunks, static_cast<S *>(y));
-    return cudaGetLastError();
+    const int packs = H / VEC;
+    const auto launch = [&](auto lanes_c, auto threads_c) {
+        constexpr int LANES = decltype(lanes_c)::value, THREADS = decltype(threads_c)::value;
+        int chunk = packs, chunks = 1;
+        if (LANES == THREADS)
+            split_row(packs, T, num_sms, THREADS, chunk, chunks);
+        const int tokens = THREADS / LANES;
+        auto kernel = k <= 4   ? unsort_kernel<S, VEC, 4, LANES, THREADS>
+                      : k <= 8 ? unsort_kernel<S, VEC, 8, LANES, THREADS>
+                               : unsort_kernel<S, VEC, 0, LANES, THREADS>;
+        kernel<<<static_cast<unsigned>(static_cast<int64_t>((T + tokens - 1) / tokens) * chunks), THREADS, 0, stream>>>(
+            static_cast<const S *>(rows), slot_of, w, static_cast<const S *>(add), T, k, static_cast<int64_t>(T) * k, H,
+            chunk, chunks, static_cast<S *>(y));
+        return cudaGetLastError();
+    };
+    using std::integral_constant;
+    if (packs <= 8)
+        return launch(integral_constant<int, 8>{}, integral_constant<int, 128>{});
+    if (packs <= 64 || (packs <= 160 && T >= 16 * num_sms))
+        return launch(integral_constant<int, 32>{}, integral_constant<int, 128>{});
+    return launch(integral_constant<int, 128>{}, integral_constant<int, 128>{});
 }
 
 template <typename S, int VEC>
@@ -842,17 +919,30 @@ cudaError_t unsort_backward_vec(const void *dy, const void *rows, const int32_t 
     const S *g = static_cast<const S *>(dy), *r = static_cast<const S *>(rows);
     S *d = static_cast<S *>(drows);
     const int64_t N = static_cast<int64_t>(T) * k;
+    const int packs = H / VEC;
+    const auto entries = [&](auto lanes_c) {
+        constexpr int LANES = decltype(lanes_c)::value;
+        const int64_t blocks = (N * LANES + kBackThreads - 1) / kBackThreads;
+        unsort_backward_kernel<S, VEC, LANES><<<static_cast<unsigned>(blocks), kBackThreads, 0, stream>>>(
+            g, r, slot_of, w, k, N, H, d, dw);
+        return cudaGetLastError();
+    };
+    const auto tokens = [&](auto jb) {
+        constexpr int JB = decltype(jb)::value, THREADS = JB == 1 ? kBackThreads : 64;
+        unsort_backward_token_kernel<S, VEC, JB, THREADS>
+            <<<dim3(T, (k + JB - 1) / JB), THREADS, 0, stream>>>(g, r, slot_of, w, k, N, H, d, dw);
+        return cudaGetLastError();
+    };
     if (N < 8 * static_cast<int64_t>(num_sms))
-        unsort_backward_token_kernel<S, VEC, 1>
-            <<<dim3(T, k), kBackThreads, 0, stream>>>(g, r, slot_of, w, k, N, H, d, dw);
-    else if (VEC * sizeof(S) == 16 && H / VEC >= kBackThreads && T >= 2 * num_sms)
-        unsort_backward_token_kernel<S, VEC, 8>
-            <<<dim3(T, (k + 7) / 8), kBackThreads, 0, stream>>>(g, r, slot_of, w, k, N, H, d, dw);
-    else
-        unsort_backward_kernel<S, VEC>
-            <<<static_cast<unsigned>((N + kBackThreads / 32 - 1) / (kBackThreads / 32)), kBackThreads, 0, stream>>>(
-                g, r, slot_of, w, k, N, H, d, dw);
-    return cudaGetLastError();
+        return tokens(std::integral_constant<int, 1>{});
+    if (packs <= 8)
+        return entries(std::integral_constant<int, 8>{});
+    if (packs <= 64 && k > 1 && T >= 2 * num_sms) {
+        if (k <= 4)
+            return tokens(std::integral_constant<int, 4>{});
+        return tokens(std::integral_constant<int, 8>{});
+    }
+    return entries(std::integral_constant<int, 32>{});
 }
 
 template <typename S, int VEC>
