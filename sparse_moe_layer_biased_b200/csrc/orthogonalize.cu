@@ -27,6 +27,7 @@
 //
 // Sums are fp32 (the tensor cores' accumulators); |u|_F is summed in 64 bits in a fixed order, so
 // neither range nor order matters. No atomics: the same input gives the same bits.
+#include <atomic>
 #include <cmath>
 
 #include <cuda_fp16.h>
@@ -848,6 +849,305 @@ cudaError_t launch_gemm(const CUtensorMap &a_km, const CUtensorMap &a_mn, const 
                             b_km, b_mn, em, a, dc.wait);
 }
 
+__device__ __forceinline__ uint32_t cluster_nctarank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ float4 dsmem_ld_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// ---------------------------------------------------------------------- products split over K
+// Products of few tiles: a cluster of C CTAs per 128 x 128 tile, each with its share of the K slices; the
+// parts are summed through distributed shared memory in rank order, each CTA a share of the tile's rows, with the same
+// arithmetic behind as in epi_part. A tile on the diagonal of A or B loads its slices once. What bounds such products
+// is the way through one tile, so both the K loop and the epilogue get shorter: 1 x 256 x 4096 (A: 3 tiles of
+// 64 slices) 199 -> 108 us a call, 1 x 1000 x 1000 178 -> 136, 4 x 200 x 600 119 -> 100.
+constexpr int kSplitThreads = 512;
+constexpr int kSplitMaxC = 8;
+constexpr uint32_t kSplitRed = OrthGeo<false>::kStages * OrthGeo<false>::kStageBytes;  // this CTA's part, fp32
+constexpr uint32_t kSplitBar = kSplitRed + 128 * 128 * 4;
+constexpr uint32_t kSplitSmem = kSplitBar + 8 * (2 * OrthGeo<false>::kStages + 1) + 16 + 1024;
+static_assert(kSplitSmem <= static_cast<uint32_t>(kMaxDynSmem), "shared memory");
+
+struct SplitArgs {
+    const __half *old_hi, *old_lo;  // what the epilogue multiplies in (A; X), NULL for A's product
+    __half *hi, *lo;                // the result; lo NULL for B
+    int64_t pitch, mat;             // of all of them, elements
+};
+
+template <int KIND, bool TALL>
+__global__ void __launch_bounds__(kSplitThreads, 1)
+    orth_split_kernel(const __grid_constant__ CUtensorMap a_km, const __grid_constant__ CUtensorMap a_mn,
+                      const __grid_constant__ CUtensorMap b_km, const __grid_constant__ CUtensorMap b_mn,
+                      const OrthArgs a, const SplitArgs sp, const WaitCfg wc)
+{
+    using G = OrthGeo<false>;
+    constexpr int S = G::kStages;
+    // operand sources as in orth_gemm_kernel
+    constexpr bool kAsym = KIND == kSquare || (KIND == kUpdate && !TALL);
+    constexpr bool kBsym = KIND == kSquare || (KIND == kUpdate && TALL);
+    constexpr bool kAmn = KIND == kGram && TALL;
+    constexpr bool kBmn = (KIND == kGram && TALL) || (KIND == kUpdate && !TALL);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float *red = reinterpret_cast<float *>(smem + kSplitRed);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kSplitBar);
+    uint64_t *empty = full + S, *done = empty + S;
+    uint32_t *holder = reinterpret_cast<uint32_t *>(done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(holder + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int C = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
+    allow_dependents();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_map(&a_km);
+        tma_prefetch_map(&a_mn);
+        tma_prefetch_map(&b_km);
+        tma_prefetch_map(&b_mn);
+    }
+    if (warp == 1) {
+        tmem_alloc(holder, 128);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    dependency_wait();
+    const uint32_t tmem = *holder;
+    const int M = KIND == kUpdate ? a.rows : a.p, N = KIND == kUpdate ? a.cols : a.p;
+    const int K = KIND == kGram ? (TALL ? a.rows : a.cols) : a.p;
+    const int nm = (M + 127) / 128, nn = (N + 127) / 128, nk = (K + 63) / 64, share = (nk + C - 1) / C;
+    const int parts = (nk + share - 1) / share;  // CTAs that have slices
+    const int kb0 = rank * share, kb1 = kb0 + share < nk ? kb0 + share : nk;
+    const OrthTile t = tile_at<KIND>(blockIdx.x / C, tiles_of<KIND>(nm, nn), nm, nn);
+    const int m0 = t.ti * 128, n0 = t.tj * 128;
+    const bool one = KIND != kUpdate && t.ti == t.tj;  // both operands are the same rows
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % S;
+                if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1, wc, abort_flag))
+                    break;
+                mbar_arrive_expect_tx(&full[s], one ? G::kOperand : G::kStageBytes);
+                uint8_t *A = smem + s * G::kStageBytes;
+                const int k0 = kb * 64;
+                load_operand<false>(A, &a_km, &a_mn, smem_u32(&full[s]), m0, k0, t.mat,
+                                    kAsym ? stored_mirrored<128>(t.ti, k0) : kAmn);
+                if (!one)
+                    load_operand<false>(A + G::kOperand, &b_km, &b_mn, smem_u32(&full[s]), n0, k0, t.mat,
+                                        kBsym ? stored_mirrored<128>(t.tj, k0) : kBmn);
+            }
+            for (int i = it > S ? it - S : 0; i < it; ++i)
+                mbar_wait_drain(&full[i % S], (i / S) & 1, wc);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int it = 0;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % S;
+                if (!mbar_wait(&full[s], (it / S) & 1, wc, abort_flag))
+                    break;
+                tc_fence_after();
+                const uint32_t sa = smem_u32(smem + s * G::kStageBytes), sb = one ? sa : sa + G::kOperand;
+                const bool amn = kAsym ? stored_mirrored<128>(t.ti, kb * 64) : kAmn;
+                const bool bmn = kBsym ? stored_mirrored<128>(t.tj, kb * 64) : kBmn;
+                const uint64_t ad = amn ? sdesc_mn(sa) : sdesc_kmajor_sw128(sa);
+                const uint64_t bd = bmn ? sdesc_mn(sb) : sdesc_kmajor_sw128(sb);
+                const int as = amn ? 2048 >> 4 : 2, bs = bmn ? 2048 >> 4 : 2;
+                const uint32_t idesc = idesc_f16_f32(128, 128) | (amn ? 1u << 15 : 0u) | (bmn ? 1u << 16 : 0u);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    umma_bf16(tmem, ad + as * ks, bd + bs * ks, idesc, (it | ks) != 0);
+                umma_commit(&empty[s]);
+            }
+            umma_commit(done);
+            mbar_wait_drain(done, 0, wc);
+        }
+        __syncwarp();
+    }
+    warp_wait(done, 0, wc, abort_flag);
+    tc_fence_after();
+    // 16-byte columns rotated by the row, which keeps a column's stores off one bank
+    if (kb0 < kb1) {
+        const int r = (warp & 3) * 32 + lane, cg = warp >> 2;
+        float v[32];
+        tmem_load32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + cg * 32, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<float4 *>(red + r * 128 + ((cg * 8 + k + r) & 31) * 4) =
+                make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    constexpr bool per_row = KIND == kSquare || (KIND == kUpdate && !TALL);
+    constexpr bool per_col = KIND == kSquare || (KIND == kUpdate && TALL);
+    const float *rd = (KIND == kUpdate ? a.rb : a.ra) + t.mat * a.r_mat;  // padded to a multiple of 64
+    const bool last = KIND == kUpdate && a.out != nullptr;
+    for (int e = rank * kSplitThreads + threadIdx.x; e < 128 * 32; e += C * kSplitThreads) {
+        const int i = e >> 5, row = m0 + i, col = n0 + (e & 31) * 4;
+        if (row >= M || col >= N)  // (the columns of the last four that are not the matrix's are in its padding)
+            continue;
+        const int64_t at = t.mat * sp.mat + row * sp.pitch + col;
+        uint2 oh = make_uint2(0, 0), ol = make_uint2(0, 0);
+        float4 rest = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (KIND != kGram) {
+            oh = *reinterpret_cast<const uint2 *>(sp.old_hi + at);
+            ol = *reinterpret_cast<const uint2 *>(sp.old_lo + at);
+        }
+        if (per_col)
+            rest = *reinterpret_cast<const float4 *>(rd + col);
+        if (per_row) {
+            const float x = rd[row];
+            rest = make_float4(rest.x + x, rest.y + x, rest.z + x, rest.w + x);
+        }
+        const uint32_t from = smem_u32(red + i * 128 + (((e & 31) + i) & 31) * 4);
+        float4 v[kSplitMaxC];
+#pragma unroll
+        for (int c = 0; c < kSplitMaxC; ++c)
+            if (c < parts)
+                v[c] = dsmem_ld_f4(dsmem_addr(from, c));
+        float4 m = v[0];
+#pragma unroll
+        for (int c = 1; c < kSplitMaxC; ++c)
+            if (c < parts) {
+                m.x += v[c].x;
+                m.y += v[c].y;
+                m.z += v[c].z;
+                m.w += v[c].w;
+            }
+        const float2 o0 = join_f16(oh.x, ol.x), o1 = join_f16(oh.y, ol.y);
+        if (KIND == kGram) {
+            const float f = kSa / (kSx * kSx);
+            m = make_float4(m.x * f, m.y * f, m.z * f, m.w * f);
+        } else if (KIND == kSquare) {
+            const float f = a.c * (kSb / kSa) * (1.0f / kSa);
+            m.x = fmaf(a.b, o0.x, f * fmaf(rest.x, o0.x, m.x));
+            m.y = fmaf(a.b, o0.y, f * fmaf(rest.y, o0.y, m.y));
+            m.z = fmaf(a.b, o1.x, f * fmaf(rest.z, o1.x, m.z));
+            m.w = fmaf(a.b, o1.y, f * fmaf(rest.w, o1.y, m.w));
+        } else {
+            const float f = 1.0f / kSb;
+            m.x = fmaf(fmaf(rest.x, f, a.a), o0.x, m.x * f);
+            m.y = fmaf(fmaf(rest.y, f, a.a), o0.y, m.y * f);
+            m.z = fmaf(fmaf(rest.z, f, a.a), o1.x, m.z * f);
+            m.w = fmaf(fmaf(rest.w, f, a.a), o1.y, m.w * f);
+        }
+        uint2 h, l;
+        if (last) {
+            const __nv_bfloat162 b0 = __floats2bfloat162_rn(m.x * a.out_scale, m.y * a.out_scale);
+            const __nv_bfloat162 b1 = __floats2bfloat162_rn(m.z * a.out_scale, m.w * a.out_scale);
+            __nv_bfloat16 *o = a.out + (static_cast<int64_t>(t.mat) * M + row) * N + col;
+            if (a.out_wide) {  // N is a multiple of 8
+                *reinterpret_cast<uint2 *>(o) = make_uint2(*reinterpret_cast<const uint32_t *>(&b0),
+                                                           *reinterpret_cast<const uint32_t *>(&b1));
+            } else {
+                const __nv_bfloat16 b[4] = {b0.x, b0.y, b1.x, b1.y};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (col + k < N)
+                        o[k] = b[k];
+            }
+            continue;
+        }
+        const float2 r0 = split_pair(m.x, m.y, h.x, l.x), r1 = split_pair(m.z, m.w, h.y, l.y);
+        *reinterpret_cast<uint2 *>(sp.hi + at) = h;
+        if (KIND != kSquare)
+            *reinterpret_cast<uint2 *>(sp.lo + at) = l;
+        if (KIND != kUpdate && row >= col && row < col + 4)  // the diagonal
+            (KIND == kGram ? a.ra : a.rb)[t.mat * a.r_mat + row] =
+                row == col ? r0.x : (row == col + 1 ? r0.y : (row == col + 2 ? r1.x : r1.y));
+    }
+    cluster_sync_all();  // no CTA leaves while a peer may still read its part
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 128);
+    }
+}
+
+// Clusters of each size (2, 4, 8) that the current device runs at a time, which its groups of SMs decide. The same for
+// every product's kernel: one CTA per SM.
+struct SplitRoom {
+    int clusters[3];
+};
+
+cudaError_t split_room(SplitRoom &room)
+{
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][3];  // clusters + 1
+    int device = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    for (int i = 0; i < 3 && err == cudaSuccess; ++i) {
+        const int have = device < kDevices ? known[device][i].load(std::memory_order_relaxed) : 0;
+        if (have) {
+            room.clusters[i] = have - 1;
+            continue;
+        }
+        auto kernel = orth_split_kernel<kGram, false>;
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSplitSmem));
+        if (err != cudaSuccess)
+            break;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 << i);
+        cfg.blockDim = dim3(kSplitThreads);
+        cfg.dynamicSmemBytes = kSplitSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2 << i;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        err = cudaOccupancyMaxActiveClusters(&room.clusters[i], kernel, &cfg);
+        if (err == cudaSuccess && device < kDevices)
+            known[device][i].store(room.clusters[i] + 1, std::memory_order_relaxed);
+    }
+    return err;
+}
+
+// CTAs per tile, 0: not split. The most for which all clusters run at once and each CTA has a K slice:
+// 5 x 256 x 1000 (15 tiles by 8) 132 -> 108 us, 22 x 256 x 2000 (66 by 2) 249 -> 217 us; the 36 tiles of 12 x 256 x 256 by 4
+// are too many for one wave, 153 us, by 2 105, not split 112 us.
+int split_of(int64_t tiles, int K, const SplitRoom &room)
+{
+    for (int i = 2; i >= 0; --i)
+        if (tiles <= room.clusters[i] && (K + 63) / 64 >= 2 << i)
+            return 2 << i;
+    return 0;
+}
+
+template <int KIND, bool TALL>
+cudaError_t launch_split(int C, int64_t tiles, const CUtensorMap &a_km, const CUtensorMap &a_mn,
+                         const CUtensorMap &b_km, const CUtensorMap &b_mn, const OrthArgs &a, const SplitArgs &sp,
+                         const DeviceContext &dc, cudaStream_t stream)
+{
+    auto kernel = orth_split_kernel<KIND, TALL>;
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSplitSmem));
+    if (err != cudaSuccess)
+        return err;
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(tiles * C)), kSplitThreads, kSplitSmem, stream, C, a_km,
+                            a_mn, b_km, b_mn, a, sp, dc.wait);
+}
+
 // --------------------------------------------------------------------------- short matrices
 // p <= 128: a whole call in one launch, a cluster of C CTAs per matrix. CTA c holds columns [c W, (c + 1) W)
 // of X (rows of the input, for a tall matrix) for all steps: X in fp32 in tensor memory, one row per
@@ -883,26 +1183,9 @@ struct ShortArgs {
     double eps;
 };
 
-__device__ __forceinline__ uint32_t cluster_nctarank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-
 __device__ __forceinline__ void fence_proxy_async_all()
 {
     asm volatile("fence.proxy.async;" ::: "memory");
-}
-
-__device__ __forceinline__ float4 dsmem_ld_f4(uint32_t addr)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
 }
 
 __device__ __forceinline__ double dsmem_ld_f64(uint32_t addr)
@@ -1539,17 +1822,47 @@ moe_status_t run_steps(const moe_orthogonalize_desc &d, const OrthLayout &L, con
         ok = ok && map_stack_f16(&oe, out, d.cols, d.rows, n, d.cols, static_cast<int64_t>(d.rows) * d.cols, 32, 128);
     if (!ok)
         return MOE_ERR_CUDA;
+    const auto half = [&](size_t off) { return reinterpret_cast<__half *>(w + off); };
+    const int64_t nm = (L.p + 127) / 128, a_tiles = nm * (nm + 1) / 2 * n;
+    const int64_t x_tiles = static_cast<int64_t>((d.rows + 127) / 128) * ((d.cols + 127) / 128) * n;
+    SplitRoom room{};
+    if (!PAIR && split_room(room) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    const int gram = PAIR ? 0 : split_of(a_tiles, TALL ? d.rows : d.cols, room);
+    const int square = PAIR ? 0 : split_of(a_tiles, L.p, room);
+    const int update = PAIR ? 0 : split_of(x_tiles, L.p, room);
+    const int64_t a_pitch = L.a_pitch, a_mat = L.a_mat, x_pitch = L.x_pitch, x_mat = L.x_mat;
     cudaError_t e = cudaSuccess;
     for (int step = 0; step < d.steps && e == cudaSuccess; ++step) {
         const int cur = step & 1;
         a.out = step + 1 == d.steps ? out : nullptr;
-        e = launch_gemm<kGram, TALL, PAIR>(xk[cur], xm[cur], xk[cur], xm[cur], EpiMaps{ae, al, ae, al}, a, dc, s);
-        if (e == cudaSuccess)
-            e = launch_gemm<kSquare, TALL, PAIR>(ak, am, ak, am, EpiMaps{ae, al, be, be}, a, dc, s);
-        const EpiMaps em{xe[cur], xl, a.out ? oe : xe[cur ^ 1], xl};
-        if (e == cudaSuccess)
-            e = TALL ? launch_gemm<kUpdate, TALL, PAIR>(xk[cur], xm[cur], bk, bm, em, a, dc, s)
-                     : launch_gemm<kUpdate, TALL, PAIR>(bk, bm, xk[cur], xm[cur], em, a, dc, s);
+        if (gram) {
+            const SplitArgs sp{nullptr, nullptr, half(L.ah), half(L.al), a_pitch, a_mat};
+            e = launch_split<kGram, TALL>(gram, a_tiles, xk[cur], xm[cur], xk[cur], xm[cur], a, sp, dc, s);
+        } else {
+            const EpiMaps em{ae, al, ae, al};
+            e = launch_gemm<kGram, TALL, PAIR>(xk[cur], xm[cur], xk[cur], xm[cur], em, a, dc, s);
+        }
+        if (e != cudaSuccess)
+            break;
+        if (square) {
+            const SplitArgs sp{half(L.ah), half(L.al), half(L.bh), nullptr, a_pitch, a_mat};
+            e = launch_split<kSquare, TALL>(square, a_tiles, ak, am, ak, am, a, sp, dc, s);
+        } else {
+            const EpiMaps em{ae, al, be, be};
+            e = launch_gemm<kSquare, TALL, PAIR>(ak, am, ak, am, em, a, dc, s);
+        }
+        if (e != cudaSuccess)
+            break;
+        const CUtensorMap &lk = TALL ? xk[cur] : bk, &lm = TALL ? xm[cur] : bm;
+        const CUtensorMap &rk = TALL ? bk : xk[cur], &rm = TALL ? bm : xm[cur];
+        if (update) {
+            const SplitArgs sp{half(xh[cur]), half(L.xl), half(xh[cur ^ 1]), half(L.xl), x_pitch, x_mat};
+            e = launch_split<kUpdate, TALL>(update, x_tiles, lk, lm, rk, rm, a, sp, dc, s);
+        } else {
+            const EpiMaps em{xe[cur], xl, a.out ? oe : xe[cur ^ 1], xl};
+            e = launch_gemm<kUpdate, TALL, PAIR>(lk, lm, rk, rm, em, a, dc, s);
+        }
     }
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

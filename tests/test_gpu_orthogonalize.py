@@ -208,3 +208,16 @@ def test_many_tiles_a_cta_with_short_ones_among_them(rows, cols):
     n = 170
     g = gauss(n, rows, cols, 17)
     check(moe.Orthogonalizer(n, rows, cols).orthogonalize(g), reference(g))
+
+
+@pytest.mark.parametrize("tall", [False, True])
+@pytest.mark.parametrize("n,p,q", [(1, 129, 140), (1, 256, 1100), (2, 130, 560), (3, 260, 2049), (8, 256, 1000), (30, 200, 500),
+                                   (1, 900, 1000), (80, 200, 260), (1, 100, 4001)])
+def test_few_tiles(n, p, q, tall):
+    """Products whose K is split over clusters of two to eight CTAs, some of them without a slice, beside ones that are not."""
+    rows, cols = (q, p) if tall else (p, q)
+    g = gauss(n, rows, cols, 18)
+    o = moe.Orthogonalizer(n, rows, cols)
+    out = o.orthogonalize(g)
+    check(out, reference(g))
+    assert torch.equal(out, o.orthogonalize(g))
