@@ -353,7 +353,8 @@ MOE_API moe_status_t moe_orthogonalize_workspace_size(const moe_orthogonalize_de
 
 /* grad [n, rows, cols] of dtype; momentum [n, rows, cols] fp32, updated in place, or NULL; out
  * [n, rows, cols] bf16 bit patterns, overwritten; all contiguous and aligned to their elements,
- * ws 256-byte aligned. n = 0 is a no-op. Deterministic. */
+ * ws 256-byte aligned. Arrays must not overlap. n = 0 is a no-op. Deterministic: the same call gives the same
+ * bits (a matrix in a stack of another size may round differently). */
 MOE_API moe_status_t moe_orthogonalize(const moe_orthogonalize_desc *desc, const void *grad, float *momentum,
                                        uint16_t *out, void *ws, size_t ws_bytes, void *stream);
 

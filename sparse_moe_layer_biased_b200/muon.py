@@ -43,8 +43,8 @@ class Orthogonalizer(Caller):
     def orthogonalize(self, grad: torch.Tensor, momentum: torch.Tensor | None = None, out: torch.Tensor | None = None,
                       stream=None) -> torch.Tensor:
         """grad [n, rows, cols] of grad_dtype, momentum [n, rows, cols] fp32 (updated in place) or
-        None -> the update [n, rows, cols] bf16, in `out` if given. Runs on the current stream of the
-        tensors' device, or on `stream`."""
+        None -> the update [n, rows, cols] bf16, in `out` if given (else allocated on the current stream).
+        Runs on the current stream of the tensors' device, or on `stream`."""
         check_tensor(grad, "grad", self.shape, self.grad_dtype, self._dev)
         if momentum is not None:
             check_tensor(momentum, "momentum", self.shape, torch.float32, self._dev)

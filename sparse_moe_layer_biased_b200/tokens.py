@@ -65,8 +65,8 @@ class TokenSorter(Caller):
     elsewhere, so k may exceed E).
 
     Every method runs on the current stream of the tensors' device, or on `stream`. `out` gives
-    the results' tensors, else they are allocated; rows of a sorted array that no entry owns are
-    not written. The sorter's workspace serves one sort at a time: sorts that may overlap on
+    the results' tensors, else they are allocated on the current stream; rows of a sorted array that no
+    entry owns are not written. The sorter's workspace serves one sort at a time: sorts that may overlap on
     the GPU (two streams, two graphs replayed at once) need a sorter each, and a sorter outlives the
     graphs captured from it."""
 

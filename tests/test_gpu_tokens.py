@@ -297,3 +297,20 @@ def test_infinities_and_nan_stay_in_their_tokens():
     bad = ~torch.isfinite(y)
     assert bad.nonzero().tolist() == [[3, 5], [7, 6]]
     assert y[3, 5] == float("inf") and torch.isnan(y[7, 6])
+
+
+# widths around those where rows share a block, a warp or a few lanes; token counts that leave a block's last ones empty
+NARROW = [
+    (2403, 1064, 40, 5, BF, 0.1), (2403, 1064, 40, 12, BF, 0.1), (403, 1064, 40, 5, BF, 0.1), (2501, 264, 7, 9, HF, 0.2),
+    (1003, 90, 9, 4, BF, 0.1), (777, 45, 9, 3, BF, 0.1), (301, 64, 40, 8, HF, 0.3), (301, 64, 40, 8, FP, 0.3),
+    (2405, 130, 5, 2, FP, 0.1), (2405, 255, 40, 1, BF, 0.2), (4099, 520, 40, 1, BF, 0.0), (605, 512, 40, 4, BF, 0.1),
+    (605, 513, 40, 6, HF, 0.1), (2369, 1280, 16, 8, BF, 0.1), (2369, 1288, 16, 8, BF, 0.1), (305, 2, 3, 20, FP, 0.5),
+]
+
+
+@pytest.mark.parametrize("case", NARROW, ids=[f"T{c[0]}-H{c[1]}-k{c[3]}-{str(c[4])[6:]}" for c in NARROW])
+def test_rows_that_share_a_block(case):
+    test_sort(case)
+    for weighted in (True, False):
+        test_unsort(case, weighted, weighted)
+        test_unsort_backward(case, weighted)
