@@ -8,6 +8,7 @@ if the library is missing this module raises on import of the first call.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -124,6 +125,19 @@ def lib():
             getattr(L, name).restype = i32
         _lib = L
     return _lib
+
+
+@functools.cache
+def calls():
+    """The extension module of TokenSorter's calls (csrc/calls.cpp), bound to the loaded library."""
+    L = lib()
+    try:
+        from . import _calls
+    except ImportError as e:
+        raise RuntimeError("the extension module _calls is not built: python -m sparse_moe_layer_biased_b200.build") from e
+    _calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        L.moe_sort_tokens, L.moe_sort_tokens_backward, L.moe_unsort_tokens, L.moe_unsort_tokens_backward)))
+    return _calls
 
 
 def _p(t):

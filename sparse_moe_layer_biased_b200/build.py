@@ -6,6 +6,7 @@ sparse_moe_layer_biased_b200/libmoe_b200.so with the CUDA runtime linked statica
 The debug variant (`--debug`) compiles the same sources with MOE_DEBUG into _build/debug/
 and links libmoe_b200_debug.so: device-side range checks of every index read from device
 data, reported through moe_check_device() as MOE_ERR_DEVICE_BOUNDS.
+csrc/calls.cpp becomes the extension module _calls.so beside them (g++, PyTorch's headers).
 `python -m sparse_moe_layer_biased_b200.build [--force] [--debug] [--verbose-ptxas]`.
 """
 from __future__ import annotations
@@ -14,6 +15,7 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_b200.so")
 LIB_DEBUG = os.path.join(PKG, "libmoe_b200_debug.so")
+CALLS = os.path.join(PKG, "_calls.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -49,7 +52,31 @@ def _compile(src, verbose_ptxas, debug=False):
     return obj, r.stderr
 
 
+def build_calls(force: bool = False) -> str:
+    """The extension module of TokenSorter's calls. It uses libmoe_b200.so by addresses that it is given."""
+    src = os.path.join(CSRC, "calls.cpp")
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= _deps():
+        return CALLS
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    libs = os.path.join(base, "lib")
+    tmp = CALLS + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"), src, "-o", tmp,
+           "-L", libs, f"-Wl,-rpath,{libs}", "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False) -> str:
+    if not debug:
+        build_calls(force)
     lib = LIB_DEBUG if debug else LIB
     if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _deps():
         return lib

@@ -314,3 +314,46 @@ def test_rows_that_share_a_block(case):
     for weighted in (True, False):
         test_unsort(case, weighted, weighted)
         test_unsort_backward(case, weighted)
+
+
+def test_refusals_on_the_device():
+    """What the host tests refuse, with tensors on the device: no call is made, the error names the tensor."""
+    T, H, E, k = 12, 64, 5, 2
+    s = moe.TokenSorter(T, H, E, k)
+    x = torch.ones((T, H), dtype=BF, device="cuda")
+    idx = torch.zeros((T, k), dtype=torch.int32, device="cuda")
+    xs, offsets, slot = s.sort(x, idx)
+    w = torch.ones((T, k), device="cuda")
+    keep = xs.clone()
+    for bad in (x.half(), x.cpu(), x[:, :32], x.t().contiguous().t(), x[0]):
+        with pytest.raises(ValueError, match="x:"):
+            s.sort(bad, idx, out=(xs, offsets, slot))
+        if bad.dim() == 2:
+            with pytest.raises(ValueError, match="dy:"):
+                s.unsort_backward(bad, xs, slot, w)
+            with pytest.raises(ValueError, match="add:"):
+                s.unsort(xs, slot, w, add=bad)
+            with pytest.raises(ValueError, match="dx:"):
+                s.sort_backward(xs, slot, out=bad)
+    for bad in (idx.long(), idx.cpu(), idx[:-1], idx.flatten()):
+        with pytest.raises(ValueError, match="topk_idx"):
+            s.sort(x, bad)
+    for bad in (w.double(), w.bfloat16(), w.cpu(), w[:, :1], slot):
+        with pytest.raises(ValueError, match="topk_w"):
+            s.unsort(xs, slot, bad)
+        with pytest.raises(ValueError, match="topk_w"):
+            s.unsort_backward(x, xs, slot, bad)
+    with pytest.raises(ValueError, match="offsets"):
+        s.sort(x, idx, out=(xs, offsets[:-1], slot))
+    with pytest.raises(ValueError, match="exceed"):
+        s.sort(torch.cat([x, x]), torch.cat([idx, idx]))
+    calls = _abi.calls()
+    spec = s._spec
+    for args in ((), (spec, 0), (spec, 0, xs, slot), ((1, 2), 0, xs, slot, x), (spec, "stream", xs, slot, x)):
+        with pytest.raises(TypeError):
+            calls.sort_backward(*args)
+    assert calls.sort_backward(spec, 0, xs, slot, None) == -1 and calls.sort_backward(spec, 0, xs, x, x) == -1
+    meta = torch.empty((T, H), dtype=BF, device="meta")
+    assert calls.sort_backward(spec, 0, xs, slot, meta) == -1
+    torch.cuda.synchronize()
+    assert torch.equal(xs, keep)
