@@ -357,3 +357,9 @@ def test_refusals_on_the_device():
     assert calls.sort_backward(spec, 0, xs, slot, meta) == -1
     torch.cuda.synchronize()
     assert torch.equal(xs, keep)
+
+
+@pytest.mark.parametrize("T,E", [(2048, 31), (2049, 32), (6144, 1024), (6145, 7), (8192, 300), (8193, 300)])
+def test_sort_at_the_borders_of_its_rounds(T, E):
+    """16384, 49152 and 65536 entries, and a token more."""
+    test_sort((T, 8, E, 8, BF, 0.1))
