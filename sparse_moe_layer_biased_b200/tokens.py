@@ -49,6 +49,8 @@ class Caller:
 
     def _run(self, fn, stream, *args) -> None:
         """fn(*args, stream handle) with the device current, on `stream` or the device's current stream."""
+        if self._dev < 0:
+            raise ValueError(f"{fn.__name__}: tensors in the memory of a CUDA device are wanted")
         if self._several and torch.cuda.current_device() != self._dev:
             with torch.cuda.device(self._dev):
                 return self._run(fn, stream, *args)

@@ -172,3 +172,15 @@ def test_wrappers_refuse_on_the_host():
         o.orthogonalize(g, out=g)
     with pytest.raises(moe.MoeError):
         moe.Orthogonalizer(2, 8, 16, grad_dtype=torch.float16, device="cpu")
+
+
+def test_tensors_in_host_memory_never_reach_the_library():
+    """Calls that are right in all but the memory they are in."""
+    s = moe.TokenSorter(8, 16, 4, 2, dtype=torch.float32, device="cpu")
+    x, idx, rows = torch.zeros(8, 16), torch.zeros(8, 2, dtype=torch.int32), torch.zeros(16, 16)
+    w = torch.zeros(8, 2)
+    for call in (lambda: s.sort(x, idx), lambda: s.sort_backward(rows, idx), lambda: s.unsort(rows, idx, w, add=x),
+                 lambda: s.unsort_backward(x, rows, idx, w),
+                 lambda: moe.Orthogonalizer(2, 8, 16, device="cpu").orthogonalize(torch.zeros(2, 8, 16))):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
