@@ -321,7 +321,7 @@ struct OrthGeo {
     static constexpr uint32_t kEpiOff = kStages * kStageBytes;
     static constexpr uint32_t kBarOff = kEpiOff + kBlocks * 2 * kBlock;
     static constexpr uint32_t kMiscOff = kBarOff + 8 * (2 * kStages + 5 + 2 * kBlocks);
-    static constexpr uint32_t kSmem = kMiscOff + 16 + 1024;
+    static constexpr uint32_t kSmem = kMiscOff + 16 + 1024;  // misc: TMEM holder, abort flag, the peer's flag and stage count
     static constexpr uint32_t kTmemCols = 2 * kTile;
     static_assert(kSmem <= static_cast<uint32_t>(kMaxDynSmem), "ring exceeds shared memory");
     static_assert(kBlocks >= kGroups && (kGroups & (kGroups - 1)) == 0, "a group's blocks are kGroups apart");
@@ -362,6 +362,36 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, uin
             "[%2];" ::"r"(smem_u32(dst)),
             "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
             : "memory");
+}
+
+// Counts `bytes` of `bar`'s current phase as landed that no copy will bring.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void dsmem_st_s32(uint32_t addr, int v)
+{
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// A pair's loads still in flight after an expired wait, which count on the leader's full barriers: the leader
+// issued stages [0, mine), the peer [0, theirs), and of either at most the last S may not have landed. Neither can be
+// more than S ahead, since a stage is issued when the one S before it has been multiplied, which takes both
+// CTAs' bytes. A stage of one CTA alone would never complete its phase: the bytes that the other did not ask
+// for are counted as landed, or the stage is armed for the peer's bytes, and then its barrier waits
+// for exactly what was issued. Run by one thread of the leader once both CTAs' roles have ended.
+template <int S>
+__device__ __forceinline__ void drain_pair(uint64_t *full, int mine, int theirs, uint32_t stage_bytes, const WaitCfg &wc)
+{
+    const int most = mine > theirs ? mine : theirs;
+    for (int i = most > S ? most - S : 0; i < most; ++i) {
+        if (i >= theirs)
+            mbar_complete_tx(&full[i % S], stage_bytes);
+        else if (i >= mine)
+            mbar_arrive_expect_tx(&full[i % S], stage_bytes);
+        mbar_wait_drain(&full[i % S], (i / S) & 1, wc);
+    }
 }
 
 struct OrthTile {
@@ -551,7 +581,8 @@ struct BlockWalk {
 //
 // On CTA pairs the leader (cluster rank 0) issues the MMAs; both CTAs' loads count on the leader's
 // full barriers, the leader's commits arrive in both CTAs, and both epilogues arrive on the leader's
-// accumulator-empty barriers.
+// accumulator-empty barriers. Without an expired wait every load was multiplied and has landed with that;
+// with one in either CTA, both hear of it in the final cluster barrier, and neither leaves before drain_pair.
 template <int KIND, bool TALL, bool PAIR>
 __global__ void __launch_bounds__(OrthGeo<PAIR>::kThreads, 1)
     orth_gemm_kernel(const __grid_constant__ CUtensorMap a_km, const __grid_constant__ CUtensorMap a_mn,
@@ -576,6 +607,7 @@ __global__ void __launch_bounds__(OrthGeo<PAIR>::kThreads, 1)
     uint64_t *bdone = bfull + G::kBlocks;  // [kBlocks] its new ones are written
     uint32_t *holder = reinterpret_cast<uint32_t *>(smem + G::kMiscOff);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + G::kMiscOff + 4);
+    volatile int *peer_abort = abort_flag + 1, *peer_issued = abort_flag + 2;  // written by the pair's other CTA
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
     const uint32_t full0 = PAIR ? dsmem_addr(smem_u32(full), 0) : smem_u32(full);
@@ -596,6 +628,8 @@ __global__ void __launch_bounds__(OrthGeo<PAIR>::kThreads, 1)
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
+        *peer_abort = 0;
+        *peer_issued = 0;
         fence_barrier_init();
         tma_prefetch_map(&a_km);
         tma_prefetch_map(&a_mn);
@@ -627,9 +661,9 @@ __global__ void __launch_bounds__(OrthGeo<PAIR>::kThreads, 1)
     const int tiles = per * a.n;
     const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, stride = PAIR ? gridDim.x >> 1 : gridDim.x;
 
+    int it = 0;  // stages that the producer has issued
     if (warp == 0) {
         if (lane == 0) {
-            int it = 0;
             bool stop = false;
             for (int tile = first; tile < tiles && !stop; tile += stride) {
                 const OrthTile t = tile_at<KIND>(tile, per, nm, nn);
@@ -651,15 +685,11 @@ __global__ void __launch_bounds__(OrthGeo<PAIR>::kThreads, 1)
                                        kBsym ? stored_mirrored<TILE>(t.tj, k0) : kBmn);
                 }
             }
-            // The loads this CTA issued must have landed before it leaves. The leader's barriers
-            // count both CTAs' bytes; the peer, which cannot wait on them, leaves behind the final
-            // cluster barrier. After an abort either may have issued stages that the other did not,
-            // whose barriers never complete: both then wait 200 us, far longer than a load takes.
-            if (PAIR && (stop || *abort_flag)) {
-                const unsigned long long t0 = global_ns();
-                while (global_ns() - t0 < 200000ull) {
-                }
-            } else if (rank == 0) {
+            // the loads this CTA issued have landed before it leaves (a pair's: behind the roles)
+            if (PAIR) {
+                if (rank == 1)
+                    dsmem_st_s32(dsmem_addr(smem_u32(const_cast<const int *>(peer_issued)), 0), it);
+            } else {
                 for (int i = it > S ? it - S : 0; i < it; ++i)
                     mbar_wait_drain(&full[i % S], (i / S) & 1, wc);
             }
@@ -816,10 +846,18 @@ __global__ void __launch_bounds__(OrthGeo<PAIR>::kThreads, 1)
         }
     }
     tc_fence_before();
-    if (PAIR)
+    if (PAIR) {
+        if (*abort_flag)  // seen by the thread that set it, if by no other
+            dsmem_st_s32(dsmem_addr(smem_u32(const_cast<const int *>(peer_abort)), rank ^ 1), 1);
         cluster_sync_all();  // both CTAs are done with TMEM, shared memory and each other's barriers
-    else
+        if (*abort_flag || *peer_abort) {
+            if (threadIdx.x == 0 && rank == 0)
+                drain_pair<S>(full, it, *peer_issued, G::kStageBytes, wc);
+            cluster_sync_all();
+        }
+    } else {
         __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
         if (PAIR)
