@@ -59,3 +59,35 @@ def test_a_pair_waits_for_its_loads_not_for_a_time(n, rows, cols):
     statuses, times = expired_calls(n, rows, cols)
     assert set(statuses) == {"timeout"}
     assert min(times) < 1500, times
+
+
+@pytest.mark.parametrize("n,rows,cols", [
+    (64, 300, 900), (64, 900, 300),                  # single CTAs
+    (16, 768, 2048),                                 # CTA pairs
+    (1, 256, 1100), (1, 1100, 256), (1, 256, 4096),  # every product split over K
+])
+def test_every_form_of_the_products_reports_expired_waits(n, rows, cols):
+    statuses, _ = expired_calls(n, rows, cols)
+    assert "timeout" in statuses
+
+
+@pytest.mark.parametrize("n,rows,cols", [(40, 100, 700), (40, 700, 100), (3, 128, 2048)])
+def test_short_matrices_at_the_lowest_limit(n, rows, cols):
+    """The one-launch form waits for nothing but its own products, of at most 16 MMAs: less than the lowest limit, so
+    its waits do not have to run out; a call that reports no timeout has to be right."""
+    o = moe.Orthogonalizer(n, rows, cols)
+    g = torch.randn((n, rows, cols), device="cuda", generator=torch.Generator(device="cuda").manual_seed(23))
+    want = o.orthogonalize(g).clone()
+    old = _abi.moe_set_wait_limit_ns(1000)
+    try:
+        for _ in range(4):
+            got = o.orthogonalize(g)
+            try:
+                _abi.moe_check_device()
+            except _abi.MoeError as e:
+                assert e.status == 5, e
+                continue
+            assert torch.equal(got, want)
+    finally:
+        _abi.moe_set_wait_limit_ns(old)
+    assert torch.equal(o.orthogonalize(g), want)
