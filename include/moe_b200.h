@@ -348,7 +348,8 @@ typedef struct {
 /* MOE_ERR_UNSUPPORTED: rows or cols above 16384, n above 65535, fp16 gradients, or coefficients
  * whose iterates leave the operands' range (singular values growing past 7.9, or b*s^2 +
  * c*s^4 past 31). The workspace holds as many matrices as fit 2 GiB (at least one), 12 bytes per
- * element of X and A; larger stacks are worked off in equal chunks. */
+ * element of X and A; larger stacks are worked off in equal chunks. Matrices with a shorter side up to 128
+ * and a longer one up to 2048 are worked on without any: 256 bytes, whatever n. */
 MOE_API moe_status_t moe_orthogonalize_workspace_size(const moe_orthogonalize_desc *desc, size_t *bytes);
 
 /* grad [n, rows, cols] of dtype; momentum [n, rows, cols] fp32, updated in place, or NULL; out

@@ -1719,6 +1719,11 @@ OrthLayout orth_layout(const moe_orthogonalize_desc &d)
     OrthLayout L{};
     const size_t rows = d.rows, cols = d.cols;
     L.p = d.rows < d.cols ? d.rows : d.cols;
+    int W, C;
+    if (short_split(L.p, d.rows < d.cols ? d.cols : d.rows, W, C)) {
+        L.total = 256;  // one launch, all of it on chip: the least that a caller can hand over
+        return L;
+    }
     L.x_pitch = up(cols, 64);
     L.x_mat = rows * L.x_pitch;
     L.a_pitch = up(L.p, 64);

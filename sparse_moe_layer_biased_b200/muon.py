@@ -24,7 +24,7 @@ class Orthogonalizer(Caller):
     (nesterov) or m; X = u / (|u|_F + eps); `steps` times X <- a X + (b A + c A A) X with A = X X^T
     (of the shorter side), coeffs = (a, b, c); the update is bf16(scale X).
 
-    The workspace (up to 2 GiB, more if one matrix needs it) serves one call at a time: calls
+    The workspace (up to 2 GiB, more if one matrix needs it, none to speak of for sides up to 128 x 2048) serves one call at a time: calls
     that may overlap on the GPU (two streams, two graphs replayed at once) need an Orthogonalizer
     each, and it outlives the graphs captured from it."""
 
