@@ -7,6 +7,7 @@ if the library is missing this module raises on import of the first call.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -160,6 +161,21 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+_CURRENT = contextlib.nullcontext()
+
+
+def _allocating_on(stream, device):
+    """Context in which torch.empty gives memory for work on `stream` (None: the current one): what the memory held
+    before is then behind that work in the stream's own order, whatever the current stream still has to do with it."""
+    if stream is None:
+        return _CURRENT
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        # 0 and 1 are the default stream's handles
+        stream = torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device=device)
+    return torch.cuda.stream(stream)
 
 
 def _check(fn, st):

@@ -26,7 +26,8 @@ class Orthogonalizer(Caller):
 
     The workspace (up to 2 GiB, more if one matrix needs it, none to speak of for sides up to 128 x 2048) serves one call at a time: calls
     that may overlap on the GPU (two streams, two graphs replayed at once) need an Orthogonalizer
-    each, and it outlives the graphs captured from it."""
+    each. It belongs to the stream that was current when the Orthogonalizer was made, which outlives its calls in flight
+    on other streams and the graphs captured from it."""
 
     def __init__(self, n: int, rows: int, cols: int, grad_dtype: torch.dtype = torch.float32, steps: int = 5,
                  coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, scale: float = 1.0, beta: float = 0.95,
@@ -43,13 +44,14 @@ class Orthogonalizer(Caller):
     def orthogonalize(self, grad: torch.Tensor, momentum: torch.Tensor | None = None, out: torch.Tensor | None = None,
                       stream=None) -> torch.Tensor:
         """grad [n, rows, cols] of grad_dtype, momentum [n, rows, cols] fp32 (updated in place) or
-        None -> the update [n, rows, cols] bf16, in `out` if given (else allocated on the current stream).
+        None -> the update [n, rows, cols] bf16, in `out` if given (else allocated on the stream that the call runs on).
         Runs on the current stream of the tensors' device, or on `stream`."""
         check_tensor(grad, "grad", self.shape, self.grad_dtype, self._dev)
         if momentum is not None:
             check_tensor(momentum, "momentum", self.shape, torch.float32, self._dev)
         if out is None:
-            out = torch.empty(self.shape, dtype=torch.bfloat16, device=self.device)
+            with _abi._allocating_on(stream, self.device):
+                out = torch.empty(self.shape, dtype=torch.bfloat16, device=self.device)
         check_tensor(out, "out", self.shape, torch.bfloat16, self._dev)
         self._run(_abi.lib().moe_orthogonalize, stream, ctypes.byref(self.desc), grad.data_ptr(),
                   None if momentum is None else momentum.data_ptr(), out.data_ptr(), self.ws.data_ptr(), self.ws.numel())

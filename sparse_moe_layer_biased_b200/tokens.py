@@ -66,10 +66,10 @@ class TokenSorter(Caller):
     elsewhere, so k may exceed E).
 
     Every method runs on the current stream of the tensors' device, or on `stream`. `out` gives
-    the results' tensors, else they are allocated on the current stream; rows of a sorted array that no
-    entry owns are not written. The sorter's workspace serves one sort at a time: sorts that may overlap on
-    the GPU (two streams, two graphs replayed at once) need a sorter each, and a sorter outlives the
-    graphs captured from it."""
+    the results' tensors, else they are allocated on the stream that the method runs on; rows of a sorted array
+    that no entry owns are not written. The sorter's workspace serves one sort at a time: sorts that may overlap on
+    the GPU (two streams, two graphs replayed at once) need a sorter each. It belongs to the stream that was current
+    when the sorter was made: a sorter outlives its sorts in flight on other streams and the graphs captured from it."""
 
     def __init__(self, max_tokens: int, H: int, E: int, k: int, dtype: torch.dtype = torch.bfloat16, device="cuda"):
         if dtype not in _abi.DTYPES:
@@ -108,9 +108,10 @@ class TokenSorter(Caller):
         """x [T, H], topk_idx [T, k] int32 -> (x_sorted [T*k, H], offsets [E+1], slot_of [T, k] int32)."""
         T, H, k, dt = x.shape[0], self.H, self.k, self.dtype
         if out is None:
-            out = (torch.empty((T * k, H), dtype=dt, device=self.device),
-                   torch.empty(self.E + 1, dtype=torch.int32, device=self.device),
-                   torch.empty((T, k), dtype=torch.int32, device=self.device))
+            with _abi._allocating_on(stream, self.device):
+                out = (torch.empty((T * k, H), dtype=dt, device=self.device),
+                       torch.empty(self.E + 1, dtype=torch.int32, device=self.device),
+                       torch.empty((T, k), dtype=torch.int32, device=self.device))
         x_sorted, offsets, slot_of = out
         status = self._call(self._calls.sort, stream, x, topk_idx, x_sorted, offsets, slot_of)
         if status:
@@ -123,7 +124,8 @@ class TokenSorter(Caller):
         """dx_sorted [T*k, H] -> dx [T, H], the sum of each token's rows."""
         T, H, k, dt = slot_of.shape[0], self.H, self.k, self.dtype
         if out is None:
-            out = torch.empty((T, H), dtype=dt, device=self.device)
+            with _abi._allocating_on(stream, self.device):
+                out = torch.empty((T, H), dtype=dt, device=self.device)
         status = self._call(self._calls.sort_backward, stream, dx_sorted, slot_of, out)
         if status:
             self._refuse("moe_sort_tokens_backward", status, (
@@ -135,7 +137,8 @@ class TokenSorter(Caller):
         and summed, plus add [T, H] (None: 0)."""
         T, H, k, dt = slot_of.shape[0], self.H, self.k, self.dtype
         if out is None:
-            out = torch.empty((T, H), dtype=dt, device=self.device)
+            with _abi._allocating_on(stream, self.device):
+                out = torch.empty((T, H), dtype=dt, device=self.device)
         status = self._call(self._calls.unsort, stream, y_sorted, slot_of, topk_w, add, out)
         if status:
             self._refuse("moe_unsort_tokens", status, (
@@ -148,8 +151,9 @@ class TokenSorter(Caller):
         """dy [T, H] -> (dy_sorted [T*k, H], dtopk_w [T, k] fp32). The gradient of unsort's `add` is dy."""
         T, H, k, dt = slot_of.shape[0], self.H, self.k, self.dtype
         if out is None:
-            out = (torch.empty((T * k, H), dtype=dt, device=self.device),
-                   torch.empty((T, k), dtype=torch.float32, device=self.device))
+            with _abi._allocating_on(stream, self.device):
+                out = (torch.empty((T * k, H), dtype=dt, device=self.device),
+                       torch.empty((T, k), dtype=torch.float32, device=self.device))
         dy_sorted, dtopk_w = out
         status = self._call(self._calls.unsort_backward, stream, dy, y_sorted, slot_of, topk_w, dy_sorted, dtopk_w)
         if status:
