@@ -35,12 +35,13 @@ class MoeLayer:
         if T > self.max_tokens:
             raise ValueError(f"{T} tokens exceed the workspace size of {self.max_tokens}")
         desc = _abi.desc_of(self.shape, T=T, deterministic=self.deterministic)
-        if y is None:
-            y = torch.empty((T, self.shape.H), dtype=torch.float32, device=x.device)
         idx = w = None
-        if routing:
-            idx = torch.empty((T, self.shape.k), dtype=torch.int32, device=x.device)
-            w = torch.empty((T, self.shape.k), dtype=torch.float32, device=x.device)
+        with _abi._allocating_on(stream, x.device):
+            if y is None:
+                y = torch.empty((T, self.shape.H), dtype=torch.float32, device=x.device)
+            if routing:
+                idx = torch.empty((T, self.shape.k), dtype=torch.int32, device=x.device)
+                w = torch.empty((T, self.shape.k), dtype=torch.float32, device=x.device)
         W = self.w
         if self.fp8:
             _abi.moe_forward_fp8(desc, x, W["Wr"], W["bias"], W["W_gate_up_q"], W["W_gate_up_s"], W["W_down_q"],
@@ -61,7 +62,9 @@ class MoeLayer:
         desc = _abi.desc_of(self.shape, T=T, deterministic=self.deterministic)
         need = _abi.moe_host_workspace_size(desc)
         if getattr(self, "ws_host", None) is None or self.ws_host.numel() < need:
-            self.ws_host = torch.empty(need, dtype=torch.uint8, device=self.w["Wr"].device)
+            dev = self.w["Wr"].device
+            with _abi._allocating_on(stream, dev):
+                self.ws_host = torch.empty(need, dtype=torch.uint8, device=dev)
         if y_host is None:
             y_host = torch.empty((n, T, H), dtype=torch.float32, pin_memory=True)
         W = self.w
