@@ -4,17 +4,19 @@
 //
 // Each function takes spec = (max_tokens, H, E, k, moe_dtype_t, device index, workspace address, workspace
 // bytes), the stream's handle and the tensors (None where the C entry point takes NULL), and returns the
-// entry point's status, or kNotWanted if a tensor is not of the shape, type, device and layout that spec and the
-// others call for; the caller then says which.
+// entry point's status, kNotWanted if a tensor is not of the shape, type, device and layout that spec and the
+// others call for, or kWantsGradient if autograd is recording and one requires a gradient, which the call would lose;
+// the caller then says which.
 #include <Python.h>
 
+#include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/moe_b200.h"
 
 namespace {
 
-constexpr long kNotWanted = -1;
+constexpr long kNotWanted = -1, kWantsGradient = -2;
 
 decltype(&moe_sort_tokens) sort_fn;
 decltype(&moe_sort_tokens_backward) sort_backward_fn;
@@ -82,6 +84,16 @@ bool token_count(PyObject *o, Spec &s)
     return true;
 }
 
+bool wants_gradient(PyObject *const *t, Py_ssize_t n)
+{
+    if (!c10::GradMode::is_enabled())
+        return false;
+    for (Py_ssize_t i = 0; i < n; ++i)
+        if (THPVariable_Check(t[i]) && THPVariable_Unpack(t[i]).requires_grad())
+            return true;
+    return false;
+}
+
 // body(spec, stream, tensors) -> status, with Python's and C++'s errors turned into kNotWanted.
 template <typename Body>
 PyObject *call(PyObject *const *a, Py_ssize_t n, Py_ssize_t tensors, Body body)
@@ -101,7 +113,9 @@ PyObject *call(PyObject *const *a, Py_ssize_t n, Py_ssize_t tensors, Body body)
         void *stream = PyLong_AsVoidPtr(a[1]);
         if (!stream && PyErr_Occurred())
             return nullptr;
-        if (s.device >= 0)
+        if (wants_gradient(a + 2, tensors))
+            status = kWantsGradient;
+        else if (s.device >= 0)
             status = body(s, stream, a + 2);
     } catch (...) {  // a tensor without memory
         PyErr_Clear();

@@ -22,7 +22,7 @@ from .tokens import Caller, check_tensor
 class Orthogonalizer(Caller):
     """n matrices [rows, cols]: u = grad, or with momentum m <- beta m + grad and u = grad + beta m
     (nesterov) or m; X = u / (|u|_F + eps); `steps` times X <- a X + (b A + c A A) X with A = X X^T
-    (of the shorter side), coeffs = (a, b, c); the update is bf16(scale X).
+    (of the shorter side), coeffs = (a, b, c); the update is bf16(scale X). Autograd does not record it.
 
     The workspace (up to 2 GiB, more if one matrix needs it, none to speak of for sides up to 128 x 2048) serves one call at a time: calls
     that may overlap on the GPU (two streams, two graphs replayed at once) need an Orthogonalizer

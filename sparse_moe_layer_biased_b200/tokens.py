@@ -12,6 +12,9 @@ layer whose experts are computed elsewhere:
     dx_sorted = experts_backward(dy_sorted, offsets)
     dx = sorter.sort_backward(dx_sorted, slot_of)
 
+Autograd does not record these calls: inside torch.autograd.Function (or under torch.no_grad()) they take any tensor,
+while autograd is recording they refuse one that requires a gradient.
+
 PyTorch only allocates device memory and supplies the stream; the arithmetic runs in libmoe_b200.so. A small call's
 kernel is over in 2.5 us, so the extension module _calls checks the tensors and makes the call: 3 us of host time, of which
 the launch takes 2.3; the checks in Python and ctypes took 6.5.
@@ -94,7 +97,12 @@ class TokenSorter(Caller):
         return fn(self._spec, _abi._raw_stream(self._dev) if stream is None else _abi._stream(stream), *tensors)
 
     def _refuse(self, name: str, status: int, wanted, sorted_tokens: int = 0) -> None:
-        """The error of a call: for status -1 that of the tensor which is not as wanted, (tensor, name, shape, dtype)."""
+        """The error of a call: for status -1 that of the tensor which is not as wanted, (tensor, name, shape, dtype); for -2
+        that of the one which requires a gradient."""
+        if status == -2:
+            names = ", ".join(what for tensor, what, _, _ in wanted if tensor is not None and tensor.requires_grad)
+            raise ValueError(f"{name}: {names}: requires a gradient, but autograd does not record this call; make it inside "
+                             "torch.autograd.Function or under torch.no_grad(), and take gradients with the _backward methods")
         if status < 0:
             for tensor, what, shape, dtype in wanted:
                 if tensor is not None:
