@@ -10,6 +10,8 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -131,11 +133,16 @@ def lib():
 @functools.cache
 def calls():
     """The extension module of TokenSorter's calls (csrc/calls.cpp), bound to the loaded library."""
-    L = lib()
-    try:
-        from . import _calls
-    except ImportError as e:
-        raise RuntimeError("the extension module _calls is not built: python -m sparse_moe_layer_biased_b200.build") from e
+    from .build import calls_path
+
+    L, path = lib(), calls_path()
+    if not os.path.exists(path):
+        raise RuntimeError(f"the extension module {os.path.basename(path)} is not built: "
+                           "python -m sparse_moe_layer_biased_b200.build")
+    name = f"{__package__}._calls"
+    spec = importlib.util.spec_from_loader(name, importlib.machinery.ExtensionFileLoader(name, path))
+    _calls = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(_calls)
     _calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         L.moe_sort_tokens, L.moe_sort_tokens_backward, L.moe_unsort_tokens, L.moe_unsort_tokens_backward)))
     return _calls

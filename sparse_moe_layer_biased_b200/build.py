@@ -6,7 +6,8 @@ sparse_moe_layer_biased_b200/libmoe_b200.so with the CUDA runtime linked statica
 The debug variant (`--debug`) compiles the same sources with MOE_DEBUG into _build/debug/
 and links libmoe_b200_debug.so: device-side range checks of every index read from device
 data, reported through moe_check_device() as MOE_ERR_DEVICE_BOUNDS.
-csrc/calls.cpp becomes the extension module _calls.so beside them (g++, PyTorch's headers).
+csrc/calls.cpp becomes the extension module _calls-torch<version>.<Python's ABI>.so beside them (g++, PyTorch's
+headers), which TokenSorter alone needs: where it cannot be built, a warning says so and the library is there.
 `python -m sparse_moe_layer_biased_b200.build [--force] [--debug] [--verbose-ptxas]`.
 """
 from __future__ import annotations
@@ -16,6 +17,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,7 +25,6 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_b200.so")
 LIB_DEBUG = os.path.join(PKG, "libmoe_b200_debug.so")
-CALLS = os.path.join(PKG, "_calls.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -52,16 +53,26 @@ def _compile(src, verbose_ptxas, debug=False):
     return obj, r.stderr
 
 
+def calls_path() -> str:
+    """Where the extension module for this PyTorch and Python is: one built for others is not loaded by them."""
+    import torch
+
+    return os.path.join(PKG, f"_calls-torch{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build_calls(force: bool = False) -> str:
     """The extension module of TokenSorter's calls. It uses libmoe_b200.so by addresses that it is given."""
-    src = os.path.join(CSRC, "calls.cpp")
-    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= _deps():
-        return CALLS
+    src, out = os.path.join(CSRC, "calls.cpp"), calls_path()
+    fresh = os.path.exists(out) and os.path.getmtime(out) >= _deps()
+    if fresh and not force:
+        return out
+    if not fresh and os.path.exists(out):
+        os.remove(out)  # not to be loaded with a newer library, should the build fail
     import torch
 
     base = os.path.dirname(torch.__file__)
     libs = os.path.join(base, "lib")
-    tmp = CALLS + ".tmp"
+    tmp = out + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
            "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(base, "include"),
@@ -70,13 +81,20 @@ def build_calls(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
-    return CALLS
+    os.replace(tmp, out)
+    return out
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False) -> str:
-    if not debug:
+    lib = build_library(force, verbose_ptxas, debug)
+    try:
         build_calls(force)
+    except (OSError, RuntimeError) as e:
+        warnings.warn(f"TokenSorter's extension module is not built, all else is: {e}", RuntimeWarning, stacklevel=2)
+    return lib
+
+
+def build_library(force: bool = False, verbose_ptxas: bool = False, debug: bool = False) -> str:
     lib = LIB_DEBUG if debug else LIB
     if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _deps():
         return lib
