@@ -19,6 +19,10 @@ from . import _abi
 from .tokens import Caller, check_tensor
 
 
+def _orthogonalize(desc, stream, *args) -> int:
+    return _abi.lib().moe_orthogonalize(desc, *args, stream)
+
+
 class Orthogonalizer(Caller):
     """n matrices [rows, cols]: u = grad, or with momentum m <- beta m + grad and u = grad + beta m
     (nesterov) or m; X = u / (|u|_F + eps); `steps` times X <- a X + (b A + c A A) X with A = X X^T
@@ -53,6 +57,11 @@ class Orthogonalizer(Caller):
             with _abi._allocating_on(stream, self.device):
                 out = torch.empty(self.shape, dtype=torch.bfloat16, device=self.device)
         check_tensor(out, "out", self.shape, torch.bfloat16, self._dev)
-        self._run(_abi.lib().moe_orthogonalize, stream, ctypes.byref(self.desc), grad.data_ptr(),
-                  None if momentum is None else momentum.data_ptr(), out.data_ptr(), self.ws.data_ptr(), self.ws.numel())
+        status = self._call(_orthogonalize, stream, ctypes.byref(self.desc), grad.data_ptr(),
+                            None if momentum is None else momentum.data_ptr(), out.data_ptr(), self.ws.data_ptr(),
+                            self.ws.numel())
+        if status < 0:
+            raise ValueError("moe_orthogonalize: tensors in the memory of a CUDA device are wanted")
+        if status:
+            raise _abi.MoeError("moe_orthogonalize", status)
         return out

@@ -50,16 +50,15 @@ class Caller:
         self.device = torch.device("cpu") if self._dev < 0 else torch.device("cuda", self._dev)
         self._several = torch.cuda.device_count() > 1
 
-    def _run(self, fn, stream, *args) -> None:
-        """fn(*args, stream handle) with the device current, on `stream` or the device's current stream."""
+    def _call(self, fn, stream, plan, *args) -> int:
+        """Status of fn(plan, stream handle, *args) with the device current, on `stream` or the device's current stream;
+        -1 on the host."""
         if self._dev < 0:
-            raise ValueError(f"{fn.__name__}: tensors in the memory of a CUDA device are wanted")
+            return -1
         if self._several and torch.cuda.current_device() != self._dev:
             with torch.cuda.device(self._dev):
-                return self._run(fn, stream, *args)
-        status = fn(*args, _abi._raw_stream(self._dev) if stream is None else _abi._stream(stream))
-        if status:
-            raise _abi.MoeError(fn.__name__, status)
+                return self._call(fn, stream, plan, *args)
+        return fn(plan, _abi._raw_stream(self._dev) if stream is None else _abi._stream(stream), *args)
 
 
 class TokenSorter(Caller):
@@ -87,15 +86,6 @@ class TokenSorter(Caller):
     def _desc(self, T: int) -> _abi.TokenDesc:
         return _abi.TokenDesc(T, self.H, self.E, self.k, _abi.DTYPES[self.dtype])
 
-    def _call(self, fn, stream, *tensors) -> int:
-        """Status of a function of the extension module, with the device current, on `stream` or the device's current one."""
-        if self._dev < 0:
-            return -1
-        if self._several and torch.cuda.current_device() != self._dev:
-            with torch.cuda.device(self._dev):
-                return self._call(fn, stream, *tensors)
-        return fn(self._spec, _abi._raw_stream(self._dev) if stream is None else _abi._stream(stream), *tensors)
-
     def _refuse(self, name: str, status: int, wanted, sorted_tokens: int = 0) -> None:
         """The error of a call: for status -1 that of the tensor which is not as wanted, (tensor, name, shape, dtype); for -2
         that of the one which requires a gradient."""
@@ -121,7 +111,7 @@ class TokenSorter(Caller):
                        torch.empty(self.E + 1, dtype=torch.int32, device=self.device),
                        torch.empty((T, k), dtype=torch.int32, device=self.device))
         x_sorted, offsets, slot_of = out
-        status = self._call(self._calls.sort, stream, x, topk_idx, x_sorted, offsets, slot_of)
+        status = self._call(self._calls.sort, stream, self._spec, x, topk_idx, x_sorted, offsets, slot_of)
         if status:
             self._refuse("moe_sort_tokens", status, (
                 (x, "x", (T, H), dt), (topk_idx, "topk_idx", (T, k), torch.int32), (x_sorted, "x_sorted", (T * k, H), dt),
@@ -134,7 +124,7 @@ class TokenSorter(Caller):
         if out is None:
             with _abi._allocating_on(stream, self.device):
                 out = torch.empty((T, H), dtype=dt, device=self.device)
-        status = self._call(self._calls.sort_backward, stream, dx_sorted, slot_of, out)
+        status = self._call(self._calls.sort_backward, stream, self._spec, dx_sorted, slot_of, out)
         if status:
             self._refuse("moe_sort_tokens_backward", status, (
                 (slot_of, "slot_of", (T, k), torch.int32), (dx_sorted, "dx_sorted", (T * k, H), dt), (out, "dx", (T, H), dt)))
@@ -147,7 +137,7 @@ class TokenSorter(Caller):
         if out is None:
             with _abi._allocating_on(stream, self.device):
                 out = torch.empty((T, H), dtype=dt, device=self.device)
-        status = self._call(self._calls.unsort, stream, y_sorted, slot_of, topk_w, add, out)
+        status = self._call(self._calls.unsort, stream, self._spec, y_sorted, slot_of, topk_w, add, out)
         if status:
             self._refuse("moe_unsort_tokens", status, (
                 (slot_of, "slot_of", (T, k), torch.int32), (y_sorted, "y_sorted", (T * k, H), dt),
@@ -163,7 +153,8 @@ class TokenSorter(Caller):
                 out = (torch.empty((T * k, H), dtype=dt, device=self.device),
                        torch.empty((T, k), dtype=torch.float32, device=self.device))
         dy_sorted, dtopk_w = out
-        status = self._call(self._calls.unsort_backward, stream, dy, y_sorted, slot_of, topk_w, dy_sorted, dtopk_w)
+        status = self._call(self._calls.unsort_backward, stream, self._spec, dy, y_sorted, slot_of, topk_w, dy_sorted,
+                            dtopk_w)
         if status:
             self._refuse("moe_unsort_tokens_backward", status, (
                 (slot_of, "slot_of", (T, k), torch.int32), (dy, "dy", (T, H), dt), (y_sorted, "y_sorted", (T * k, H), dt),
