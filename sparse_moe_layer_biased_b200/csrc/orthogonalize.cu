@@ -8,7 +8,7 @@
 //   X <- a X + B X,  B = b A + c A A,  A = X X^T           (rows <= cols)
 //   X <- a X + X B,  A = X^T X                              (rows > cols)   `steps` times
 //   out = bf16(scale X)
-// 2 p p q + p p p multiply-adds a step for the two symmetric products' triangles and the update:
+// 3 p p q + p p p flops a step, the two symmetric products counted on and above the diagonal:
 // the tensor cores bound it, so each of the three products is a tcgen05 GEMM with the rest of the
 // step in its epilogue.
 //
