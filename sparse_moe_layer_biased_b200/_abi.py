@@ -176,7 +176,7 @@ _CURRENT = contextlib.nullcontext()
 def _allocating_on(stream, device):
     """Context in which torch.empty gives memory for work on `stream` (None: the current one): what the memory held
     before is then behind that work in the stream's own order, whatever the current stream still has to do with it."""
-    if stream is None:
+    if stream is None or torch.device(device).type != "cuda":
         return _CURRENT
     if not isinstance(stream, torch.cuda.Stream):
         handle = _stream(stream)
