@@ -27,7 +27,7 @@ def test_results_are_not_in_memory_that_the_current_stream_still_writes(handle):
     held = [torch.empty_like(t).fill_(1) for t in want for _ in range(3)]
     torch.cuda._sleep(1)
     torch.cuda.synchronize()
-    torch.cuda._sleep(200_000_000)  # 0.1 s of the current stream
+    torch.cuda._sleep(800_000_000)  # 0.4 s of the current stream
     for t in held:
         t.fill_(77)
     del held, t
@@ -59,7 +59,7 @@ def test_host_batches_on_a_given_stream():
     held = [torch.empty(size, dtype=torch.uint8, device="cuda").fill_(1) for _ in range(3)]
     torch.cuda._sleep(1)
     torch.cuda.synchronize()
-    torch.cuda._sleep(200_000_000)
+    torch.cuda._sleep(800_000_000)
     for t in held:
         t.fill_(77)
     del held, t
